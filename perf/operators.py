@@ -290,10 +290,11 @@ def _plan(st):
     free[place[back]] = table[back]
     top = n_free + given.sum()
     # pages from the top, in request order; a request that they do not reach takes no part
-    need = torch.where(ended, 0, (cached + new + P - 1) // P - have)
-    upto = torch.cumsum(need, 0)
     q_end = torch.cumsum(new, 0)
-    part = ~ended & ((need == 0) | (upto <= top)) & (cached + new <= width * P) & (q_end <= N)
+    fits = ~ended & (cached + new <= width * P) & (q_end <= N)
+    need = torch.where(fits, (cached + new + P - 1) // P - have, 0)
+    upto = torch.cumsum(need, 0)
+    part = fits & ((need == 0) | (upto <= top))
     take = part[:, None] & (col >= have[:, None]) & (col < (have + need)[:, None])
     order = (upto - need)[:, None] + col - have[:, None]
     table[take] = free[(top - 1 - order)[take]]
