@@ -39,7 +39,7 @@
  *  - Data-dependent anomalies found on the device (an index in `idx` that
  *    is out of range, a window ring too small for the query positions) never
  *    trap: the offending row is skipped and a bit is OR-ed into `*status`
- *    (dev, nullable, int32): LCSC_DEV_BAD_INDEX, LCSC_DEV_BAD_LENGTH.
+ *    (dev, nullable, int32): the LCSC_DEV_* bits below.
  *  - Batched arrays are dense: sequence b of a [B][n][...] array starts at
  *    b * n * (row bytes).  Every pointer must be 16-byte aligned.
  *  - Sequence lengths: `ctx_len` (dev, int32 [B]) gives, per sequence, the
@@ -60,7 +60,7 @@
 extern "C" {
 #endif
 
-#define LCSC_ABI_VERSION 3
+#define LCSC_ABI_VERSION 4
 
 /* Return codes. */
 #define LCSC_OK 0
@@ -73,7 +73,8 @@ extern "C" {
 #define LCSC_DEV_BAD_INDEX 1       /* an index outside [0, N(p)) was skipped */
 #define LCSC_DEV_BAD_LENGTH 2      /* a ctx_len smaller than T, or past the sizes of the call */
 #define LCSC_DEV_TIMEOUT 4         /* a kernel gave up a bounded wait (the call's results are not valid) */
-#define LCSC_DEV_RANGE 8           /* reserved: no call of this version raises it */
+#define LCSC_DEV_RANGE 8           /* a row given to lcsc_paged_store held a value that is not finite (stored as 0) */
+#define LCSC_DEV_NO_PAGES 16       /* lcsc_page_plan: the free pages did not reach every request */
 
 /* What the sink of a layer is (lcsc_params.sink_mode); "DeepSeek V4
  * Architecture Explained", "How compress-then-sparsify attention works": a
@@ -436,6 +437,139 @@ int32_t lcsc_topk_merge(const lcsc_params* p, int32_t n_parts, const int32_t* pa
 int32_t lcsc_attn_merge(const lcsc_params* p, int32_t n_parts, const void* part_out, const float* part_lse,
                         const float* sink, const int32_t* ctx_len, int64_t B, int64_t T, void* out,
                         float* lse, void* stream);
+
+/* -------------------------------------------- raw tokens in an 8-bit paged cache
+ * Ordinary attention over the raw tokens of many requests of different
+ * lengths, for what a server runs beside the compressed layers: short
+ * contexts ("How DeepSeek V4 Handles 1M Token Context": below about 8K tokens
+ * plain attention wins) and plain or sliding-window layers of the same stack.
+ * K and V lie in pages of P tokens in E4M3, with one float32 scale for each
+ * page and KV head.  One serving step is
+ *   lcsc_page_plan   block table, slots and lengths from the requests' token counts;
+ *   lcsc_paged_store the new tokens' K and V rows into their slots;
+ *   lcsc_paged_attn  the new tokens' queries over the cached tokens.
+ * The requests' new tokens lie one after another in arrays of n_tokens rows:
+ * request b has the rows q_start[b] .. q_start[b + 1] - 1.  ctx_len is the
+ * array that the other calls of this library take (length after the step).
+ * The pool (dev): k, v [n_pages][Hkv][P][D] E4M3 codes, 16-byte aligned;
+ * k_scale, v_scale [n_pages][Hkv] float32.  Token t of a request lies at row
+ * t % P of page block_table[b][t / P]; its value is code * scale.  The int32 and
+ * float32 arrays of this section need the alignment of their type only.
+ * Scale rule: the least power of two s with amax <= 448 s (not below 2^-100).
+ * Powers of two keep the relative precision of E4M3 and make a scale that
+ * grows with later tokens exact for the codes already there, except those
+ * that fall below E4M3's normal range (they are rounded once more). */
+typedef struct lcsc_paged_params {
+  int32_t n_heads;     /* Hq query heads */
+  int32_t n_kv_heads;  /* Hkv, a divisor of Hq: query head h reads KV head h / (Hq / Hkv) */
+  int32_t head_dim;    /* D: 64 or 128 */
+  int32_t page_size;   /* P: 16, 32, 64 or 128 */
+  int32_t q_dtype;     /* LCSC_DT_*: queries and output */
+  int32_t x_dtype;     /* LCSC_DT_*: K and V rows given to the store */
+  float sm_scale;      /* softmax scale of q.K (> 0) */
+  int32_t window;      /* > 0: a query sees the last `window` tokens only, its own included; 0: all */
+  float softcap;       /* c > 0: scores are capped to c tanh(score / c); 0: off */
+} lcsc_paged_params;
+
+typedef struct lcsc_paged_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t n_pages;     /* n_pages * P < 2^31 */
+} lcsc_paged_cache;
+
+/* One step's plan, on the device.  cached, n_new [B]: tokens of each request
+ * already cached, and its new ones; n_new < 0: the request has ended.
+ *   block_table [B][max_blocks] (in, out): the first ceil(cached / P) entries
+ *     of a row are its pages; entries for the new tokens are filled in, no
+ *     other is touched.
+ *   free_pages [n_pages] (in, out): a stack of n_free[0] free pages.  The
+ *     pages of the ended requests go on top of it first, in request order;
+ *     then the requests take the pages they need from the top, in request
+ *     order.  n_free_out[0]: the stack's height afterwards (may be n_free
+ *     itself; where it is not, calling again with the same n_free gives the
+ *     same plan).
+ *   ctx_len [B] = cached + n_new; q_start [B + 1]: first row of each request;
+ *   slots, positions (nullable) [n_tokens]: of each row its slot, page * P +
+ *     row in the page, and its position in the request.
+ * A request takes no part (ctx_len 0, slots and positions -1, no page taken,
+ * its row of the table as it was) when it has ended, when the free pages do not
+ * reach it (LCSC_DEV_NO_PAGES; requests after it that need a page take no part
+ * either), or when its length is negative or passes max_blocks * P or its rows
+ * pass n_tokens (LCSC_DEV_BAD_LENGTH).  Rows from q_start[B] on get slot and
+ * position -1.  A stack that would grow past n_pages drops the pages above
+ * (LCSC_DEV_BAD_INDEX).  workspace: lcsc_page_plan_workspace_size() bytes. */
+int32_t lcsc_page_plan_workspace_size(int64_t B, size_t* bytes);
+int32_t lcsc_page_plan(int32_t page_size, int64_t B, int64_t n_tokens, int64_t max_blocks, int64_t n_pages,
+                       const int32_t* cached, const int32_t* n_new, int32_t* block_table,
+                       int32_t* free_pages, const int32_t* n_free, int32_t* n_free_out, int32_t* ctx_len,
+                       int32_t* q_start, int32_t* slots, int32_t* positions, void* workspace,
+                       size_t workspace_bytes, int32_t* status, void* stream);
+
+/* K and V rows of new tokens into their slots.  k, v (dev): x_dtype rows of
+ * Hkv * D values, 16-byte aligned, `*_stride` values from one token's row to
+ * the next (a multiple of 16 bytes, at least Hkv * D), so that both may be
+ * slices of one projection's output.  slots (dev) [n_tokens] int32; a negative
+ * slot skips its row.
+ * For each page written, s' = max(the page's scale, s(amax of the new rows)),
+ * the page's old scale counting only if its first row (slot % P = 0) is not
+ * among the new ones; codes in rows before the new ones are re-encoded when
+ * the scale grows; code = E4M3_rne(x / s').  Rows of a page after the new ones
+ * keep their codes.  A value that is not finite is stored as 0 and left out of
+ * amax (LCSC_DEV_RANGE).
+ * The tokens of one page are adjacent and in rising slot order, as
+ * lcsc_page_plan gives them.  A slot outside the pool, or one that follows its
+ * neighbour within a page out of that order (the same slot twice, say), is
+ * skipped (LCSC_DEV_BAD_INDEX); a page visited again further on gets one
+ * visit's rows or the other's in each place. */
+int32_t lcsc_paged_store(const lcsc_paged_params* p, const lcsc_paged_cache* cache, const void* k, int64_t k_stride,
+                         const void* v, int64_t v_stride, const int32_t* slots, int64_t n_tokens,
+                         int32_t* status, void* stream);
+
+/* Attention of the new tokens over the cached ones (their own K and V among
+ * them).  The query of token i of request b, head h, sits at position
+ * p = ctx_len[b] - (q_start[b + 1] - q_start[b]) + i and sees the positions
+ *   max(0, p - window + 1, doc_start[row]) <= j < min(ctx_len[b], max(p + 1, prefix_len[b])),
+ * with
+ *   x_j = sm_scale q . K_j;   x_j = c tanh(x_j / c) if softcap;   x_j -= slopes[h] |p - j|;
+ *   out = sum_j e^{x_j} V_j / (e^{sink[h]} + sum_j e^{x_j}),  lse = log of the denominator.
+ * A query that sees nothing gets zeros, and lse -inf without a sink (sink[h]
+ * with one).  A request whose ctx_len is 0 takes no part: its rows get zeros
+ * and -inf.  Rows from q_start[B] on are left as they were.  A request with
+ * 0 < ctx_len < its new tokens, ctx_len < 0 or ctx_len > max_blocks * P gets
+ * zeros and -inf (LCSC_DEV_BAD_LENGTH); rows of a q_start that falls or passes
+ * n_tokens are not written (LCSC_DEV_BAD_LENGTH).  A page number outside the
+ * pool hides its tokens (LCSC_DEV_BAD_INDEX); pages that no query of the step
+ * sees are not looked at.  Codes of visible tokens are never 0x7F or 0xFF (the
+ * store writes none); rows of a page past the request's end may hold anything.
+ * BF16 queries run on the tensor cores with float32 sums: the query is the sum
+ * of E4M3 terms (values below 2^-10 of a head's largest keep an absolute
+ * precision of 2^-17 of it), the softmax weights are held to 11 bits or more;
+ * V components keep an absolute precision of 2^-17 or better of the largest
+ * |V| that the query's pages can hold.  F32 queries run in float32 throughout. */
+typedef struct lcsc_paged_batch {
+  int64_t B, n_tokens;
+  int64_t max_new;             /* >= 1: the most new tokens of one request, if known, else n_tokens; it decides
+                                  the kernel's form only: no result depends on its being right */
+  int64_t max_blocks;          /* block_table row length */
+  const int32_t* q_start;      /* [B + 1] */
+  const int32_t* ctx_len;      /* [B] */
+  const int32_t* block_table;  /* [B][max_blocks] */
+  const void* q;               /* [n_tokens] rows of Hq * D values, 16-byte aligned */
+  int64_t q_stride;            /* values from one row to the next, a multiple of 16 bytes */
+  void* out;                   /* [n_tokens][Hq][D] q_dtype */
+  float* lse;                  /* [n_tokens][Hq] or NULL */
+  const float* slopes;         /* [Hq] or NULL: bias by distance */
+  const float* sink;           /* [Hq] or NULL */
+  const int32_t* prefix_len;   /* [B] or NULL: tokens of a prefix that every query sees whole */
+  const int32_t* doc_start;    /* [n_tokens] or NULL: first position of each row's document */
+} lcsc_paged_batch;
+
+int32_t lcsc_paged_attn_workspace_size(const lcsc_paged_params* p, int64_t B, int64_t n_tokens, int64_t max_new,
+                                       size_t* bytes);
+int32_t lcsc_paged_attn(const lcsc_paged_params* p, const lcsc_paged_batch* batch, const lcsc_paged_cache* cache,
+                        void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -8,6 +8,7 @@
 
 #include "kernels.cuh"
 #include "launches.h"
+#include "paged.cuh"
 
 namespace lcsc {
 
@@ -204,6 +205,66 @@ int64_t new_entries_max(int64_t T, int m) { return T / m + 1; }
 void plan_compress(const lcsc_params* p, int64_t B, int64_t n_new, int dim, Carve& cv, float** pooled) {
   float* pl = cv.take<float>((size_t)B * (n_new > 0 ? n_new : 1) * dim);
   if (pooled) *pooled = pl;
+}
+
+// ------------------------------------------------------- paged 8-bit cache
+
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
+int log2_of(int32_t x) {
+  int l = 0;
+  while ((1 << l) < x) ++l;
+  return l;
+}
+
+bool valid_page(int32_t page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+bool valid_dt(int32_t dt) { return dt == LCSC_DT_F32 || dt == LCSC_DT_BF16; }
+int dt_bytes(int32_t dt) { return dt == LCSC_DT_F32 ? 4 : 2; }
+
+int32_t check_paged(const lcsc_paged_params* p) {
+  if (!p) return LCSC_ERR_INVALID_ARG;
+  if (p->n_heads < 1 || p->n_kv_heads < 1 || p->n_heads % p->n_kv_heads) return LCSC_ERR_INVALID_ARG;
+  if (!valid_dt(p->q_dtype) || !valid_dt(p->x_dtype)) return LCSC_ERR_INVALID_ARG;
+  if (!(p->sm_scale > 0.f) || p->sm_scale == INFINITY || p->window < 0) return LCSC_ERR_INVALID_ARG;
+  if (!(p->softcap >= 0.f) || p->softcap == INFINITY) return LCSC_ERR_INVALID_ARG;
+  if (!valid_page(p->page_size) || (p->head_dim != 64 && p->head_dim != 128)) return LCSC_ERR_UNSUPPORTED;
+  if (p->n_heads > 65535) return LCSC_ERR_UNSUPPORTED;
+  return LCSC_OK;
+}
+
+int32_t check_pool(const lcsc_paged_params* p, const lcsc_paged_cache* c) {
+  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale) return LCSC_ERR_INVALID_ARG;
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(c->k_scale) || !aligned4(c->v_scale)) return LCSC_ERR_INVALID_ARG;
+  if (c->n_pages < 1 || c->n_pages > (int64_t)INT32_MAX / p->page_size) return LCSC_ERR_INVALID_ARG;
+  // rows of all heads are counted in 32 bits by the tile loads
+  if (c->n_pages * p->page_size > (int64_t)INT32_MAX / p->n_kv_heads) return LCSC_ERR_UNSUPPORTED;
+  return LCSC_OK;
+}
+
+// A row array: `heads` * D values a row, 16-byte aligned rows.
+int32_t check_rows(const void* x, int64_t stride, int64_t values, int32_t dt) {
+  if (!x || !aligned16(x) || stride < values || stride > ((int64_t)1 << 40)) return LCSC_ERR_INVALID_ARG;
+  if ((stride * dt_bytes(dt)) % 16) return LCSC_ERR_INVALID_ARG;
+  return LCSC_OK;
+}
+
+// Query rows (tokens x heads) are counted in 32 bits.
+bool paged_sizes(const lcsc_paged_params* p, int64_t B, int64_t n_tokens, int64_t max_new) {
+  return B >= 1 && B <= (1 << 20) && n_tokens >= 0 && n_tokens <= ((int64_t)1 << 30) / p->n_heads && max_new >= 1;
+}
+
+PagedForm plan_paged(const lcsc_paged_params* p, int64_t max_new, Carve& cv, PagedLaunch* L) {
+  const PagedForm f = paged_form(p->q_dtype, p->head_dim, p->n_heads / p->n_kv_heads, max_new);
+  float* po = cv.take<float>((size_t)2 * f.ctas * f.rows * p->head_dim);
+  float* pml = cv.take<float>((size_t)2 * f.ctas * f.rows * 2);
+  int32_t* meta = cv.take<int32_t>((size_t)8 * f.ctas);
+  if (L) {
+    L->part_o = po;
+    L->part_ml = pml;
+    L->meta = meta;
+    L->ctas = f.ctas;
+  }
+  return f;
 }
 
 }  // namespace
@@ -772,6 +833,155 @@ int32_t lcsc_csa_decode(const lcsc_params* p, const lcsc_step* s, void* ws, size
 int32_t lcsc_hca_decode(const lcsc_params* p, const lcsc_step* s, void* ws, size_t ws_bytes,
                         int32_t* status, void* stream) {
   return step_impl(p, s, ws, ws_bytes, status, stream, false);
+}
+
+// ------------------------------------------------------- paged 8-bit cache
+
+int32_t lcsc_page_plan_workspace_size(int64_t B, size_t* bytes) {
+  if (!bytes || B < 1 || B > (1 << 20)) return LCSC_ERR_INVALID_ARG;
+  Carve cv{nullptr};
+  cv.take<int64_t>((size_t)B + 2);
+  *bytes = cv.used;
+  return LCSC_OK;
+}
+
+int32_t lcsc_page_plan(int32_t page_size, int64_t B, int64_t n_tokens, int64_t max_blocks, int64_t n_pages,
+                       const int32_t* cached, const int32_t* n_new, int32_t* block_table,
+                       int32_t* free_pages, const int32_t* n_free, int32_t* n_free_out, int32_t* ctx_len,
+                       int32_t* q_start, int32_t* slots, int32_t* positions, void* workspace,
+                       size_t workspace_bytes, int32_t* status, void* stream) {
+  size_t need = 0;
+  int32_t st = lcsc_page_plan_workspace_size(B, &need);
+  if (st) return st;
+  if (!valid_page(page_size)) return LCSC_ERR_UNSUPPORTED;
+  if (n_tokens < 0 || n_tokens > INT32_MAX || max_blocks < 1 || n_pages < 1) return LCSC_ERR_INVALID_ARG;
+  if (max_blocks > INT32_MAX / page_size || n_pages > INT32_MAX / page_size) return LCSC_ERR_INVALID_ARG;
+  if (!cached || !n_new || !block_table || !free_pages || !n_free || !n_free_out || !ctx_len || !q_start)
+    return LCSC_ERR_INVALID_ARG;
+  if (n_tokens > 0 && !slots) return LCSC_ERR_INVALID_ARG;
+  const void* all[] = {cached, n_new, block_table, free_pages, n_free, n_free_out, ctx_len, q_start, slots, positions};
+  for (const void* q : all)
+    if (!aligned4(q)) return LCSC_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < need) return LCSC_ERR_WORKSPACE;
+  PagePlanLaunch L;
+  L.page = page_size;
+  L.page_log2 = log2_of(page_size);
+  L.B = (int)B;
+  L.n_tokens = n_tokens;
+  L.max_blocks = max_blocks;
+  L.n_pages = n_pages;
+  L.cached = cached;
+  L.n_new = n_new;
+  L.table = block_table;
+  L.free_pages = free_pages;
+  L.n_free = n_free;
+  L.n_free_out = n_free_out;
+  L.ctx_len = ctx_len;
+  L.q_start = q_start;
+  L.slots = slots;
+  L.positions = positions;
+  L.scratch = reinterpret_cast<int64_t*>(workspace);
+  L.status = status;
+  cudaError_t e = launch_page_plan(L, (cudaStream_t)stream);
+  return e == cudaSuccess ? LCSC_OK : cuda_fail(e);
+}
+
+int32_t lcsc_paged_store(const lcsc_paged_params* p, const lcsc_paged_cache* cache, const void* k, int64_t k_stride,
+                         const void* v, int64_t v_stride, const int32_t* slots, int64_t n_tokens,
+                         int32_t* status, void* stream) {
+  int32_t st = check_paged(p);
+  if (st) return st;
+  if ((st = check_pool(p, cache))) return st;
+  if (n_tokens < 0 || n_tokens > INT32_MAX) return LCSC_ERR_INVALID_ARG;
+  if (n_tokens == 0) return LCSC_OK;
+  const int64_t values = (int64_t)p->n_kv_heads * p->head_dim;
+  if ((st = check_rows(k, k_stride, values, p->x_dtype))) return st;
+  if ((st = check_rows(v, v_stride, values, p->x_dtype))) return st;
+  if (!slots || !aligned4(slots)) return LCSC_ERR_INVALID_ARG;
+  PagedStoreLaunch L;
+  L.codes[0] = reinterpret_cast<uint8_t*>(cache->k);
+  L.codes[1] = reinterpret_cast<uint8_t*>(cache->v);
+  L.scale[0] = cache->k_scale;
+  L.scale[1] = cache->v_scale;
+  L.x[0] = k;
+  L.x[1] = v;
+  L.stride[0] = k_stride;
+  L.stride[1] = v_stride;
+  L.x_dtype = p->x_dtype;
+  L.Hkv = p->n_kv_heads;
+  L.D = p->head_dim;
+  L.page = p->page_size;
+  L.page_log2 = log2_of(p->page_size);
+  L.n_pages = cache->n_pages;
+  L.n_tokens = n_tokens;
+  L.slots = slots;
+  L.status = status;
+  cudaError_t e = launch_paged_store(L, (cudaStream_t)stream);
+  return e == cudaSuccess ? LCSC_OK : cuda_fail(e);
+}
+
+int32_t lcsc_paged_attn_workspace_size(const lcsc_paged_params* p, int64_t B, int64_t n_tokens, int64_t max_new,
+                                       size_t* bytes) {
+  int32_t st = check_paged(p);
+  if (st) return st;
+  if (!bytes || !paged_sizes(p, B, n_tokens, max_new)) return LCSC_ERR_INVALID_ARG;
+  Carve cv{nullptr};
+  plan_paged(p, max_new, cv, nullptr);
+  *bytes = cv.used;
+  return LCSC_OK;
+}
+
+int32_t lcsc_paged_attn(const lcsc_paged_params* p, const lcsc_paged_batch* s, const lcsc_paged_cache* cache, void* ws,
+                        size_t ws_bytes, int32_t* status, void* stream) {
+  int32_t st = check_paged(p);
+  if (st) return st;
+  if ((st = check_pool(p, cache))) return st;
+  if (!s || !paged_sizes(p, s->B, s->n_tokens, s->max_new)) return LCSC_ERR_INVALID_ARG;
+  if (s->max_blocks < 1 || s->max_blocks > INT32_MAX / p->page_size) return LCSC_ERR_INVALID_ARG;
+  if (!s->q_start || !s->ctx_len || !s->block_table) return LCSC_ERR_INVALID_ARG;
+  const void* small[] = {s->q_start, s->ctx_len, s->block_table, s->lse, s->slopes, s->sink, s->prefix_len, s->doc_start};
+  for (const void* q : small)
+    if (!aligned4(q)) return LCSC_ERR_INVALID_ARG;
+  if (s->n_tokens == 0) return LCSC_OK;
+  if ((st = check_rows(s->q, s->q_stride, (int64_t)p->n_heads * p->head_dim, p->q_dtype))) return st;
+  if (!s->out || !aligned16(s->out)) return LCSC_ERR_INVALID_ARG;
+  Carve cv{reinterpret_cast<uint8_t*>(ws)};
+  PagedLaunch L;
+  memset(&L, 0, sizeof(L));
+  const PagedForm f = plan_paged(p, s->max_new, cv, &L);
+  if (!ws || !aligned16(ws) || ws_bytes < cv.used) return LCSC_ERR_WORKSPACE;
+  L.q = s->q;
+  L.q_stride = s->q_stride;
+  L.q_dtype = p->q_dtype;
+  L.Hq = p->n_heads;
+  L.Hkv = p->n_kv_heads;
+  L.G = p->n_heads / p->n_kv_heads;
+  L.D = p->head_dim;
+  L.page = p->page_size;
+  L.page_log2 = log2_of(p->page_size);
+  L.k = reinterpret_cast<uint8_t*>(cache->k);
+  L.v = reinterpret_cast<uint8_t*>(cache->v);
+  L.k_scale = cache->k_scale;
+  L.v_scale = cache->v_scale;
+  L.n_pages = cache->n_pages;
+  L.B = (int)s->B;
+  L.n_tokens = s->n_tokens;
+  L.max_blocks = s->max_blocks;
+  L.q_start = s->q_start;
+  L.ctx_len = s->ctx_len;
+  L.table = s->block_table;
+  L.slopes = s->slopes;
+  L.sink = s->sink;
+  L.prefix = s->prefix_len;
+  L.docs = s->doc_start;
+  L.sm_scale = p->sm_scale;
+  L.cap = p->softcap;
+  L.window = p->window;
+  L.out = s->out;
+  L.lse = s->lse;
+  L.status = status;
+  cudaError_t e = launch_paged_attn(L, f, (cudaStream_t)stream);
+  return e == cudaSuccess ? LCSC_OK : cuda_fail(e);
 }
 
 }  // extern "C"

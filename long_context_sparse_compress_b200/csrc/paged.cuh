@@ -1,0 +1,364 @@
+// The paged 8-bit cache's attention: the launch's arguments, the rows and keys
+// of a request, and the schedule that every form of the kernel walks.
+//
+// An item is (request, KV head, block of M query rows), a query row being one
+// (new token, head of the group) pair, row = token * G + head in group.  An
+// item's keys are cut into tiles of TK; a unit is one tile of one item.  All
+// units of a call, in the order (request, head, row block, tile), are shared
+// out evenly over the CTAs, CTA c taking the units [U c / C, U (c + 1) / C):
+// lengths differ by orders of magnitude between the requests of a batch and are
+// known on the device only, so an even split of tiles is the one that keeps
+// every SM busy without the host knowing them.  A CTA's share is a run of
+// pieces; a piece that covers its item whole writes the output, the others
+// (at most two of a CTA: the one that ends an item begun by an earlier CTA, and
+// the one that begins an item that goes on) leave (O, max, sum) in the
+// workspace, which therefore does not grow with the lengths, and
+// paged_combine_kernel joins them in CTA order.
+#pragma once
+
+#include "common.cuh"
+
+namespace lcsc {
+
+struct PagedLaunch {
+  const void* q;
+  int64_t q_stride;  // values from one token's row to the next
+  int q_dtype;
+  int Hq, Hkv, G, D;
+  int page, page_log2;
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t n_pages;
+  int B;
+  int64_t n_tokens, max_blocks;
+  const int32_t* q_start;
+  const int32_t* ctx_len;
+  const int32_t* table;
+  const float* slopes;
+  const float* sink;
+  const int32_t* prefix;
+  const int32_t* docs;
+  float sm_scale, cap;
+  int window;
+  void* out;
+  float* lse;
+  int32_t* status;
+  // workspace: of CTA c the unfinished pieces 2c (ends an item begun before)
+  // and 2c + 1 (begins an item that goes on), and what its piece 2c belongs to
+  float* part_o;   // [2 * ctas][rows per item][D], not normalised
+  float* part_ml;  // [2 * ctas][rows per item][2]: max (base-2 units), sum
+  int32_t* meta;   // [ctas][8]
+  int ctas;
+};
+
+struct PagedStoreLaunch {
+  uint8_t* codes[2];  // K, V
+  float* scale[2];
+  const void* x[2];
+  int64_t stride[2];
+  int x_dtype, Hkv, D, page, page_log2;
+  int64_t n_pages, n_tokens;
+  const int32_t* slots;
+  int32_t* status;
+};
+
+struct PagePlanLaunch {
+  int page, page_log2, B;
+  int64_t n_tokens, max_blocks, n_pages;
+  const int32_t *cached, *n_new;
+  int32_t *table, *free_pages;
+  const int32_t* n_free;
+  int32_t *n_free_out, *ctx_len, *q_start, *slots, *positions;
+  int64_t* scratch;  // [2 + B]: stack height after the returns, unused, pages taken by earlier requests
+  int32_t* status;
+};
+
+cudaError_t launch_page_plan(const PagePlanLaunch& a, cudaStream_t stream);
+cudaError_t launch_paged_store(const PagedStoreLaunch& a, cudaStream_t stream);
+
+// The form of the attention kernel that serves a call (from the host's
+// arguments alone), its rows per item and the CTAs it launches.
+struct PagedForm {
+  int kind;  // 0: float32 on the CUDA cores
+  int rows;
+  int ctas;
+};
+PagedForm paged_form(int q_dtype, int D, int G, int64_t max_new);
+cudaError_t launch_paged_attn(const PagedLaunch& a, const PagedForm& f, cudaStream_t stream);
+
+#ifdef __CUDACC__
+
+constexpr float kPagedLog2e = 1.4426950408889634f;
+constexpr float kPagedLn2 = 0.6931471805599453f;
+
+// 2^x on the MUFU unit.
+__device__ __forceinline__ float paged_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+struct PagedSeq {
+  int64_t q0;  // first row
+  int n;       // rows' tokens (0: nothing to write)
+  int L;       // length; 0: its rows get zeros
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedLaunch& a, int b) {
+  PagedSeq s;
+  const int32_t q0 = a.q_start[b], q1 = a.q_start[b + 1];
+  int32_t L = a.ctx_len[b];
+  const bool rows_ok = q0 >= 0 && q1 >= q0 && q1 <= a.n_tokens;
+  const int n = rows_ok ? q1 - q0 : 0;
+  const bool len_ok = L == 0 || (L >= n && L <= a.max_blocks * a.page);
+  s.q0 = q0;
+  s.n = n;
+  s.L = len_ok ? L : 0;
+  if ((!rows_ok || !len_ok) && a.status) atomicOr(a.status, LCSC_DEV_BAD_LENGTH);
+  return s;
+}
+
+// Visible positions [lo, hi) of token i of a request (its document apart).
+__device__ __forceinline__ void paged_span(const PagedLaunch& a, const PagedSeq& s, int prefix, int i, int* lo,
+                                           int* hi) {
+  if (s.L == 0) {
+    *lo = *hi = 0;
+    return;
+  }
+  const int p = s.L - s.n + i;
+  *hi = min(s.L, max(p + 1, prefix));
+  *lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
+}
+
+__device__ __forceinline__ int paged_prefix(const PagedLaunch& a, int b) { return a.prefix ? a.prefix[b] : 0; }
+
+// Tiles [t0, t1) of keys that the row block mt of M rows may see; at least one.
+template <int M, int TK>
+__device__ __forceinline__ void paged_tiles(const PagedLaunch& a, const PagedSeq& s, int prefix, int mt, int* t0,
+                                            int* t1) {
+  const int rows = s.n * a.G;
+  int lo, hi, x;
+  paged_span(a, s, prefix, mt * M / a.G, &lo, &x);
+  paged_span(a, s, prefix, (min(rows, (mt + 1) * M) - 1) / a.G, &x, &hi);
+  *t0 = lo / TK;
+  *t1 = max(*t0 + 1, (hi + TK - 1) / TK);
+}
+
+// Units of one request and head.
+template <int M, int TK>
+__device__ __forceinline__ int64_t paged_units(const PagedLaunch& a, int b) {
+  const PagedSeq s = paged_seq(a, b);
+  const int prefix = paged_prefix(a, b);
+  int64_t u = 0;
+  for (int mt = 0; mt * M < s.n * a.G; ++mt) {
+    int t0, t1;
+    paged_tiles<M, TK>(a, s, prefix, mt, &t0, &t1);
+    u += t1 - t0;
+  }
+  return u;
+}
+
+// Where a CTA's share begins, found once by the whole CTA.
+struct PagedStart {
+  int64_t total;  // units of the call
+  int64_t first;  // of the request the share begins in
+  int b;
+};
+
+// CTA `cta` of `ctas` that have work (no more of them than units).
+struct PagedShare {
+  int64_t total;
+  int ctas;
+  __device__ __forceinline__ int64_t begin(int c) const { return total * c / ctas; }
+  __device__ __forceinline__ int owner(int64_t u) const { return (int)(((u + 1) * ctas - 1) / total); }
+};
+
+// Every thread of the CTA calls it; scan: shared, 34 values.  A CTA beyond
+// the last with work gets b = -1.
+template <int M, int TK>
+__device__ __forceinline__ PagedStart paged_start(const PagedLaunch& a, PagedShare* share, int64_t* scan) {
+  const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nthr >> 5;
+  auto inclusive = [&](int64_t v) {  // over the CTA's threads; scan[32]: their sum
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t w = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += w;
+    }
+    __syncthreads();
+    if (lane == 31) scan[warp] = v;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+    for (int w = 0; w < warps; ++w) {
+      if (w < warp) before += scan[w];
+      all += scan[w];
+    }
+    __syncthreads();
+    scan[32] = all;
+    return v + before;
+  };
+  PagedStart st;
+  int64_t mine = 0;
+  for (int b = tid; b < a.B; b += nthr) mine += paged_units<M, TK>(a, b) * a.Hkv;
+  inclusive(mine);
+  __syncthreads();
+  st.total = scan[32];
+  st.b = -1;
+  st.first = 0;
+  share->total = st.total;
+  share->ctas = (int)min((int64_t)gridDim.x, st.total);
+  if ((int)blockIdx.x >= share->ctas) return st;  // the same for the whole CTA
+  const int64_t u0 = share->begin(blockIdx.x);
+  int64_t base = 0;
+  __shared__ int found;
+  __shared__ int64_t found_first;
+  if (tid == 0) found = -1;
+  __syncthreads();
+  for (int b0 = 0; b0 < a.B; b0 += nthr) {
+    const int b = b0 + tid;
+    const int64_t u = b < a.B ? paged_units<M, TK>(a, b) * a.Hkv : 0;
+    const int64_t end = base + inclusive(u);
+    if (end - u <= u0 && u0 < end) {  // one thread at most
+      found = b;
+      found_first = end - u;
+    }
+    __syncthreads();
+    base += scan[32];
+    if (found >= 0) break;
+    __syncthreads();
+  }
+  st.b = found;
+  st.first = found_first;
+  return st;
+}
+
+// The pieces of a CTA's share, one after another.  Every thread that walks
+// them computes the same ones.
+template <int M, int TK>
+struct PagedWalk {
+  const PagedLaunch& a;
+  PagedShare share;
+  int64_t left;  // units still to come
+  int64_t unit;  // of the call: the next one
+  int b, h, mt, t;
+  PagedSeq s;
+  int prefix;
+  // the piece
+  int p_b, p_h, p_mt, p_t0, p_t1;
+  PagedSeq p_s;
+  bool p_head, p_tail;  // it begins / ends its item
+  int64_t p_item0, p_item1;  // units of the call of its item
+
+  __device__ __forceinline__ PagedWalk(const PagedLaunch& a_, const PagedStart& st, const PagedShare& sh)
+      : a(a_), share(sh) {
+    left = 0;
+    if (st.b < 0) return;
+    unit = share.begin(blockIdx.x);
+    left = share.begin(blockIdx.x + 1) - unit;
+    b = st.b;
+    s = paged_seq(a, b);
+    prefix = paged_prefix(a, b);
+    int64_t off = unit - st.first;
+    const int64_t per_head = paged_units<M, TK>(a, b);
+    h = (int)(off / per_head);
+    off %= per_head;
+    for (mt = 0;; ++mt) {
+      int t0, t1;
+      paged_tiles<M, TK>(a, s, prefix, mt, &t0, &t1);
+      if (off < t1 - t0) {
+        t = t0 + (int)off;
+        break;
+      }
+      off -= t1 - t0;
+    }
+  }
+
+  __device__ __forceinline__ bool next() {
+    if (left <= 0) return false;
+    int t0, t1;
+    paged_tiles<M, TK>(a, s, prefix, mt, &t0, &t1);
+    p_b = b;
+    p_h = h;
+    p_mt = mt;
+    p_s = s;
+    p_t0 = t;
+    p_t1 = (int)min((int64_t)t1, t + left);
+    p_head = t == t0;
+    p_tail = p_t1 == t1;
+    p_item0 = unit - (t - t0);
+    p_item1 = p_item0 + (t1 - t0);
+    left -= p_t1 - t;
+    unit += p_t1 - t;
+    t = p_t1;
+    if (p_tail && left > 0) {
+      if ((mt + 1) * M < s.n * a.G) {
+        ++mt;
+      } else {
+        mt = 0;
+        if (++h == a.Hkv) {
+          h = 0;
+          do {
+            s = paged_seq(a, ++b);
+          } while (s.n == 0);
+          prefix = paged_prefix(a, b);
+        }
+      }
+      paged_tiles<M, TK>(a, s, prefix, mt, &t, &t1);
+    }
+    return true;
+  }
+
+  __device__ __forceinline__ bool whole() const { return p_head && p_tail; }
+  // Where an unfinished piece goes.
+  __device__ __forceinline__ int64_t slot() const { return 2 * (int64_t)blockIdx.x + (p_head ? 1 : 0); }
+  __device__ __forceinline__ int rows() const { return min(M, p_s.n * a.G - p_mt * M); }
+
+  // What the CTA's piece 2c belongs to, for paged_combine_kernel (one thread,
+  // once the CTA's first piece is known; none: no such piece).
+  __device__ __forceinline__ void write_meta(bool none) const {
+    int32_t* m = a.meta + 8 * (int64_t)blockIdx.x;
+    if (none || p_head) {
+      m[0] = -1;
+      return;
+    }
+    m[0] = p_b;
+    m[1] = p_h;
+    m[2] = p_mt;
+    m[3] = share.owner(p_item0);
+    m[4] = share.owner(p_item1 - 1);
+  }
+};
+
+// Score of one key in base-2 units from the raw product (times its scales).
+__device__ __forceinline__ float paged_cap(float x, float cap) {
+  // c tanh(x / c) = c (1 - 2 / (e^(2x/c) + 1))
+  const float e = paged_ex2(x * (2.f * kPagedLog2e / cap));
+  return cap - __fdividef(2.f * cap, e + 1.f);
+}
+
+// One output value (row = token * G + head in group, dim d) from the sum O of
+// the weights' products, their max (base-2 units) and sum; d = 0 writes lse.
+template <int D>
+__device__ __forceinline__ void paged_write(const PagedLaunch& a, const PagedSeq& s, int h, int row, int d, float o,
+                                            float top, float l) {
+  const int head = h * a.G + row % a.G;
+  const int64_t at = (s.q0 + row / a.G) * a.Hq + head;
+  if (a.sink && s.L > 0) {
+    const float sg = a.sink[head] * kPagedLog2e, m = fmaxf(top, sg);
+    const float f = paged_ex2(top - m);  // top -inf: 0
+    if (m != -INFINITY) {
+      o *= f;
+      l = fmaf(l, f, paged_ex2(sg - m));
+      top = m;
+    }
+  }
+  const float r = l > 0.f ? o / l : 0.f;
+  if (a.q_dtype == LCSC_DT_BF16) reinterpret_cast<uint16_t*>(a.out)[at * D + d] = bf16_code(r);
+  else reinterpret_cast<float*>(a.out)[at * D + d] = r;
+  if (a.lse && d == 0) a.lse[at] = l > 0.f ? (top + log2f(l)) * kPagedLn2 : -INFINITY;
+}
+
+#endif
+
+}  // namespace lcsc

@@ -13,7 +13,7 @@ from . import workloads
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblcsc.so")
-ABI_VERSION = 3
+ABI_VERSION = 4
 
 FMT = {"f32": 0, "kv": 1, "fp8": 2, "fp4": 3}
 DT = {"f32": 0, "bf16": 1}
@@ -24,6 +24,7 @@ DEV_BAD_INDEX = 1
 DEV_BAD_LENGTH = 2
 DEV_TIMEOUT = 4
 DEV_RANGE = 8
+DEV_NO_PAGES = 16
 
 c_i32, c_i64, c_f32, c_vp, c_sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
 
@@ -51,6 +52,23 @@ class Step(ctypes.Structure):
                 ("out", c_vp), ("lse", c_vp), ("out_idx", c_vp), ("out_score", c_vp),
                 ("events", ctypes.POINTER(c_vp)), ("n_events", c_i32), ("sink_kv", Cache),
                 ("sink_v", Cache)]
+
+
+class PagedParams(ctypes.Structure):
+    _fields_ = [("n_heads", c_i32), ("n_kv_heads", c_i32), ("head_dim", c_i32), ("page_size", c_i32),
+                ("q_dtype", c_i32), ("x_dtype", c_i32), ("sm_scale", c_f32), ("window", c_i32),
+                ("softcap", c_f32)]
+
+
+class PagedPool(ctypes.Structure):
+    _fields_ = [("k", c_vp), ("v", c_vp), ("k_scale", c_vp), ("v_scale", c_vp), ("n_pages", c_i64)]
+
+
+class PagedBatch(ctypes.Structure):
+    _fields_ = [("B", c_i64), ("n_tokens", c_i64), ("max_new", c_i64), ("max_blocks", c_i64),
+                ("q_start", c_vp), ("ctx_len", c_vp), ("block_table", c_vp), ("q", c_vp), ("q_stride", c_i64),
+                ("out", c_vp), ("lse", c_vp), ("slopes", c_vp), ("sink", c_vp), ("prefix_len", c_vp),
+                ("doc_start", c_vp)]
 
 
 _SIGS = {
@@ -81,6 +99,12 @@ _SIGS = {
     "lcsc_hca_decode": (c_i32, [c_vp, c_vp, c_vp, c_sz, c_vp, c_vp]),
     "lcsc_topk_merge": (c_i32, [c_vp, c_i32, c_vp, c_vp, c_i64, c_i64, c_vp, c_vp, c_vp]),
     "lcsc_attn_merge": (c_i32, [c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_vp, c_vp, c_vp]),
+    "lcsc_page_plan_workspace_size": (c_i32, [c_i64, c_vp]),
+    "lcsc_page_plan": (c_i32, [c_i32, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                               c_vp, c_vp, c_vp, c_sz, c_vp, c_vp]),
+    "lcsc_paged_store": (c_i32, [c_vp, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp]),
+    "lcsc_paged_attn_workspace_size": (c_i32, [c_vp, c_i64, c_i64, c_i64, c_vp]),
+    "lcsc_paged_attn": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_sz, c_vp, c_vp]),
 }
 
 EXPORTS = tuple(_SIGS)
@@ -387,5 +411,158 @@ def attn_merge(p, part_out, part_lse, sink, ctx_len, out, lse=None, stream=None)
                                  ptr(out), ptr(lse), stream_handle(stream)))
 
 
+
+# -------------------------------------------------- paged 8-bit cache of raw tokens
+
+def paged_params(n_heads, n_kv_heads, head_dim, page_size, sm_scale=None, q_dtype="bf16", x_dtype="bf16", window=0,
+                 softcap=0.0):
+    """lcsc_paged_params; the softmax scale is 1 / sqrt(head_dim) unless given."""
+    return PagedParams(n_heads=n_heads, n_kv_heads=n_kv_heads, head_dim=head_dim, page_size=page_size,
+                       q_dtype=DT[q_dtype], x_dtype=DT[x_dtype],
+                       sm_scale=head_dim ** -0.5 if sm_scale is None else sm_scale, window=window, softcap=softcap)
+
+
+class PagedCache:
+    """A pool of pages in device memory: E4M3 codes of K and V,
+    [n_pages][n_kv_heads][page_size][head_dim] bytes, and a float32 scale for
+    each page and head."""
+
+    def __init__(self, n_pages, n_kv_heads, page_size, head_dim, device="cuda"):
+        shape = (n_pages, n_kv_heads, page_size, head_dim)
+        self._set(torch.zeros(shape, dtype=torch.uint8, device=device),
+                  torch.zeros(shape, dtype=torch.uint8, device=device),
+                  torch.ones(shape[:2], dtype=torch.float32, device=device),
+                  torch.ones(shape[:2], dtype=torch.float32, device=device))
+
+    @classmethod
+    def of(cls, k, v, k_scale, v_scale):
+        """A cache over tensors that are there already (codes uint8 or float8_e4m3fn)."""
+        self = cls.__new__(cls)
+        self._set(k, v, k_scale, v_scale)
+        return self
+
+    def _set(self, k, v, k_scale, v_scale):
+        for x in (k, v):
+            if x.dim() != 4 or x.shape != k.shape or x.element_size() != 1 or not x.is_contiguous():
+                raise LcscError("page codes: two contiguous 8-bit tensors [n_pages][n_kv_heads][page_size][head_dim]")
+        for x in (k_scale, v_scale):
+            if x.shape != k.shape[:2] or x.dtype != torch.float32 or not x.is_contiguous():
+                raise LcscError("page scales: two contiguous float32 tensors [n_pages][n_kv_heads]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages = k.shape[0]
+
+    def c(self):
+        return PagedPool(k=self.k.data_ptr(), v=self.v.data_ptr(), k_scale=self.k_scale.data_ptr(),
+                         v_scale=self.v_scale.data_ptr(), n_pages=self.n_pages)
+
+
+def _on_device(stream, *tensors):
+    """Every tensor (None: absent) lies on the current device, where the kernels are launched."""
+    dev = {t.get_device() for t in tensors if t is not None}
+    if stream is not None:
+        dev.add(stream.device_index)
+    if len(dev) != 1 or -1 in dev or dev.pop() != torch.cuda.current_device():
+        raise LcscError("every tensor and the stream must be on the current CUDA device")
+
+
+def _i32(name, t, n=None):
+    """An int32 array that the paged calls read or write densely."""
+    if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or (n is not None and t.numel() != n)):
+        raise LcscError(f"{name}: a contiguous int32 tensor" + ("" if n is None else f" of {n} values"))
+    return ptr(t)
+
+
+def _token_rows(name, t, heads, head_dim, dtype):
+    """Pointer and row stride (values) of a [tokens][heads][head_dim] view whose rows are dense."""
+    if t.dim() != 3 or t.shape[1:] != (heads, head_dim) or t.dtype != dtype:
+        raise LcscError(f"{name}: [tokens][{heads}][{head_dim}] of {dtype}")
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim)):
+        raise LcscError(f"{name}: the values of a token's heads must be adjacent")
+    return ptr(t), (t.stride(0) if t.shape[0] > 1 else heads * head_dim)
+
+
+_TORCH_DT = {0: torch.float32, 1: torch.bfloat16}
+
+
+def _pool_of(p, cache):
+    if tuple(cache.k.shape[1:]) != (p.n_kv_heads, p.page_size, p.head_dim):
+        raise LcscError(f"cache pages {tuple(cache.k.shape[1:])} are not the parameters' "
+                        f"({p.n_kv_heads}, {p.page_size}, {p.head_dim})")
+    return cache.c()
+
+
+def page_plan_workspace(B):
+    return _ws_size(load().lcsc_page_plan_workspace_size, B)
+
+
+def page_plan(page_size, cached, n_new, block_table, free_pages, n_free, n_free_out, ctx_len, q_start, slots,
+              positions=None, ws=None, status=None, stream=None):
+    """lcsc_page_plan: lengths, first rows, slots and block-table entries of a
+    serving step from the requests' cached and new token counts."""
+    B = cached.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise LcscError(f"block_table: [{B}][max_blocks]")
+    _on_device(stream, cached, n_new, block_table, free_pages, n_free, n_free_out, ctx_len, q_start, slots, positions,
+               ws, status)
+    if ws is None:
+        ws = workspace(page_plan_workspace(B), cached.device)
+    n = slots.numel()
+    check(load().lcsc_page_plan(
+        page_size, B, n, block_table.shape[1], free_pages.numel(), _i32("cached", cached, B),
+        _i32("n_new", n_new, B), _i32("block_table", block_table), _i32("free_pages", free_pages),
+        _i32("n_free", n_free, 1), _i32("n_free_out", n_free_out, 1), _i32("ctx_len", ctx_len, B),
+        _i32("q_start", q_start, B + 1), _i32("slots", slots), _i32("positions", positions, n), ptr(ws), ws.numel(),
+        ptr(status), stream_handle(stream)))
+    return ws
+
+
+def paged_store(p, cache, k, v, slots, status=None, stream=None):
+    """lcsc_paged_store: K and V rows [tokens][n_kv_heads][head_dim] (the
+    token stride is free) into their slots."""
+    pool = _pool_of(p, cache)
+    n = slots.numel()
+    kp, ks = _token_rows("k", k, p.n_kv_heads, p.head_dim, _TORCH_DT[p.x_dtype])
+    vp, vs = _token_rows("v", v, p.n_kv_heads, p.head_dim, _TORCH_DT[p.x_dtype])
+    if k.shape[0] != n or v.shape[0] != n:
+        raise LcscError(f"k and v: a row for each of the {n} slots")
+    _on_device(stream, cache.k, cache.v, cache.k_scale, cache.v_scale, k, v, slots, status)
+    check(load().lcsc_paged_store(ctypes.byref(p), ctypes.byref(pool), kp, ks, vp, vs, _i32("slots", slots), n,
+                                  ptr(status), stream_handle(stream)))
+
+
+def paged_attn_workspace(p, B, n_tokens, max_new):
+    return _ws_size(load().lcsc_paged_attn_workspace_size, ctypes.byref(p), B, n_tokens, max_new)
+
+
+def paged_attn(p, q, cache, block_table, ctx_len, q_start, max_new, out, lse=None, slopes=None, sink=None,
+               prefix_len=None, doc_start=None, ws=None, status=None, stream=None):
+    """lcsc_paged_attn: queries [tokens][n_heads][head_dim] (the token stride
+    is free) over the cached tokens of their requests."""
+    pool = _pool_of(p, cache)
+    n, B = q.shape[0], ctx_len.numel()
+    qp, qs = _token_rows("q", q, p.n_heads, p.head_dim, _TORCH_DT[p.q_dtype])
+    if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise LcscError("out: contiguous, of q's shape and type")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise LcscError(f"block_table: [{B}][max_blocks]")
+    for name, t, size in (("lse", lse, n * p.n_heads), ("slopes", slopes, p.n_heads), ("sink", sink, p.n_heads)):
+        if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != size):
+            raise LcscError(f"{name}: a contiguous float32 tensor of {size} values")
+    _on_device(stream, cache.k, cache.v, cache.k_scale, cache.v_scale, q, block_table, ctx_len, q_start, out, lse,
+               slopes, sink, prefix_len, doc_start, ws, status)
+    if ws is None:
+        ws = workspace(paged_attn_workspace(p, B, n, max_new), q.device)
+    batch = PagedBatch(B=B, n_tokens=n, max_new=max_new, max_blocks=block_table.shape[1], q_stride=qs)
+    for name, t in dict(q_start=_i32("q_start", q_start, B + 1), ctx_len=_i32("ctx_len", ctx_len),
+                        block_table=_i32("block_table", block_table), q=qp, out=ptr(out), lse=ptr(lse),
+                        slopes=ptr(slopes), sink=ptr(sink), prefix_len=_i32("prefix_len", prefix_len, B),
+                        doc_start=_i32("doc_start", doc_start, n)).items():
+        setattr(batch, name, t)
+    check(load().lcsc_paged_attn(ctypes.byref(p), ctypes.byref(batch), ctypes.byref(pool), ptr(ws), ws.numel(),
+                                 ptr(status), stream_handle(stream)))
+    return ws
+
+
 __all__ = ["load", "params", "DeviceCache", "compress", "encode_rows", "index_topk", "sparse_attn",
-           "dense_attn", "make_step", "decode_step", "workloads"]
+           "dense_attn", "make_step", "decode_step", "PagedCache", "paged_params", "page_plan", "paged_store",
+           "paged_attn", "workloads"]
