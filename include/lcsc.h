@@ -200,10 +200,12 @@ const char* lcsc_status_string(int32_t status);
 uint64_t lcsc_kernel_launches(void);
 /* For tests of the failure path of the bounded waits (process-wide; affects
  * calls enqueued after it returns).  limit_ns > 0: the waits of the
- * tensor-core attention and scoring kernels give up after limit_ns instead
+ * tensor-core attention (lcsc_paged_attn's among them) and scoring kernels
+ * give up after limit_ns instead
  * of 2 s.  stall != 0: in each CTA of those kernels one thread first waits on
  * a barrier that cannot complete at that point (the attention's Q K^T issuer
- * on the barrier it commits to at its end; the scoring's first lane on the
+ * on the barrier it commits to at its end, and so the paged attention's; the
+ * scoring's first lane on the
  * drain of its first accumulator, which it has not filled), so the wait runs
  * out, LCSC_DEV_TIMEOUT is set, and every role of the CTA stops, waits for
  * its copies and MMAs in flight and frees its tensor memory.  (0, 0)

@@ -660,11 +660,13 @@ cudaError_t launch_paged_store(const PagedStoreLaunch& a, cudaStream_t stream) {
 }
 
 PagedForm paged_form(int q_dtype, int D, int G, int64_t max_new) {
+  if (q_dtype == LCSC_DT_BF16) return paged_mma_form(D, G, max_new);
   return {0, kFmaRows, 4 * sm_count()};
 }
 
 cudaError_t launch_paged_attn(const PagedLaunch& a, const PagedForm& f, cudaStream_t stream) {
-  cudaError_t e = a.D == 128 ? launch_fma<128>(a, stream) : launch_fma<64>(a, stream);
+  cudaError_t e = f.kind ? launch_paged_mma(a, f, stream)
+                  : a.D == 128 ? launch_fma<128>(a, stream) : launch_fma<64>(a, stream);
   if (e != cudaSuccess || a.ctas == 1) return e;
   const dim3 grid(a.ctas, f.rows < kCombineY ? f.rows : kCombineY);
   return a.D == 128 ? launch_pdl(paged_combine_kernel<128>, grid, dim3(128), 0, stream, a, f.rows)

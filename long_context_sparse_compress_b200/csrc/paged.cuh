@@ -81,12 +81,15 @@ cudaError_t launch_paged_store(const PagedStoreLaunch& a, cudaStream_t stream);
 // The form of the attention kernel that serves a call (from the host's
 // arguments alone), its rows per item and the CTAs it launches.
 struct PagedForm {
-  int kind;  // 0: float32 on the CUDA cores
+  int kind;  // 0: float32 on the CUDA cores, 1: few rows on the tensor cores
   int rows;
   int ctas;
 };
 PagedForm paged_form(int q_dtype, int D, int G, int64_t max_new);
 cudaError_t launch_paged_attn(const PagedLaunch& a, const PagedForm& f, cudaStream_t stream);
+// The tensor-core forms (paged_mma.cu).
+PagedForm paged_mma_form(int D, int G, int64_t max_new);
+cudaError_t launch_paged_mma(const PagedLaunch& a, const PagedForm& f, cudaStream_t stream);
 
 #ifdef __CUDACC__
 

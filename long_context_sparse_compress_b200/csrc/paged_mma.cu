@@ -1,0 +1,615 @@
+// Attention over the paged 8-bit cache on the 5th-generation tensor cores, for
+// BF16 queries.  The schedule (items, units, pieces) is paged.cuh's.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "kernels.cuh"
+#include "launches.h"
+#include "paged.cuh"
+#include "sm100.cuh"
+
+namespace lcsc {
+
+using namespace sm100;
+
+namespace {
+
+// 32 lanes x N consecutive 32-bit columns of this warp's sub-partition.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld_32(taddr, r); }
+
+// Waits for this thread's tcgen05.ld with the registers passed through, so
+// that no use of them moves before the wait.
+template <int N>
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// Byte offset of (row, byte) in a swizzled block of rows of W bytes (W = 64:
+// 64-byte swizzle, W = 128: 128-byte swizzle).
+template <int W>
+__device__ __forceinline__ uint32_t swz(int row, int byte) {
+  if constexpr (W == 128) return (uint32_t)(row * 128 + ((((byte >> 4) ^ (row & 7)) << 4) | (byte & 15)));
+  else return (uint32_t)(row * 64 + ((((byte >> 4) ^ ((row >> 1) & 3)) << 4) | (byte & 15)));
+}
+template <int W>
+constexpr Swizzle kSwOf = W == 128 ? kSw128 : kSw64;
+
+// 2^e, e clamped to the normal range.
+__device__ __forceinline__ float pow2(int e) {
+  e = e < -126 ? -126 : (e > 127 ? 127 : e);
+  return __int_as_float((e + 127) << 23);
+}
+
+__device__ __forceinline__ float warp_redux_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Barrier `id` over n threads; true for all of them if `ok` is true for all.
+__device__ __forceinline__ bool named_and(int id, int n, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+
+// Bounded wait of a whole warp; false for every lane if one gave up or the CTA has.
+struct Waits {
+  int32_t* status;
+  uint64_t limit_ns;
+  volatile int* abort;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+    if (*abort) return false;
+    bool ok = mbar_wait(bar, parity, status, limit_ns);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok && (threadIdx.x & 31) == 0) *abort = 1;
+    return ok;
+  }
+};
+
+// First and past the last position that any row of a piece sees (a whole warp
+// computes it), and the first tile of the piece that holds one.
+template <int M, int TK>
+struct PieceKeys {
+  int lo, hi, t0;
+  __device__ __forceinline__ PieceKeys(const PagedLaunch& a, const PagedWalk<M, TK>& w) {
+    const int prefix = paged_prefix(a, w.p_b), r0 = w.p_mt * M, r1 = r0 + w.rows() - 1;
+    const int i0 = r0 / a.G, i1 = r1 / a.G;
+    int x;
+    paged_span(a, w.p_s, prefix, i0, &lo, &x);
+    paged_span(a, w.p_s, prefix, i1, &x, &hi);
+    if (a.docs && w.p_s.L > 0) {
+      int d = INT_MAX;
+      for (int i = i0 + (threadIdx.x & 31); i <= i1; i += 32) d = min(d, a.docs[w.p_s.q0 + i]);
+      lo = max(lo, __reduce_min_sync(0xffffffffu, d));
+    }
+    t0 = min(w.p_t1, max(w.p_t0, lo / TK));
+  }
+};
+
+// =============================================================== few rows
+// Decode steps and draft tokens: up to 32 query rows per item.  The keys lie on
+// the M side of both products, so that a tile of 128 keys is one full-height MMA
+// however few the rows are, and K and V go from TMA straight into the tensor
+// cores as they are stored:
+//   S^T [128 keys][rows] = K Q^T      K: A operand, K-major
+//   O^T [D dims][rows]   = V^T P^T    V: A operand, M-major (the same bytes)
+// Q and P, which are not stored values, are sums of E4M3 terms: two of the BF16
+// query (times a power of two per row that brings its largest value into
+// [128, 256)), three of the weights (11 bits).  One accumulating MMA chain per
+// term.  A softmax thread owns one key: maxima go over a warp with redux and
+// over the warps through shared memory.  Each tile's weights are taken against
+// the tile's own maxima, and its O is read back and added to the running one in
+// registers (a thread per dim), which is where rescaling happens: rows x 1
+// FMA per thread and tile instead of a read-modify-write of TMEM.  V's page
+// scales (powers of two) go into the weights, relative to the tile's
+// largest, so that weights always fill the E4M3 range.
+//
+// Bound: HBM (2 D bytes per key and KV head).  Per tile the tensor pipe reads
+// 5 x 16 KB of operands (640 cycles of shared memory at D = 128 against 1,420
+// cycles of HBM time); two CTAs per SM overlap one's softmax with the other's
+// copies and products.
+
+constexpr int kFewThreads = 192;  // warps 0-3 softmax, 4 copies, 5 MMA
+constexpr int kQTerms = 2, kPTerms = 3;
+
+template <int D, int NR>
+struct FewCfg {
+  static constexpr int TK = 128;
+  static constexpr int N = NR < 16 ? 16 : NR;        // MMA columns (a multiple of 16)
+  static constexpr int PW = NR <= 16 ? 64 : 128;     // bytes of a key's weights: 3 terms of N
+  static constexpr int kTile = TK * D;               // K or V bytes of a tile
+  static constexpr int kStages = D == 128 && NR == 32 ? 2 : 3;
+  static constexpr int kPerSm = 2;
+  static constexpr int kCols = NR <= 16 ? 64 : 128;  // TMEM columns: S twice, O
+  static constexpr int OFF_K = 0;
+  static constexpr int OFF_V = OFF_K + kStages * kTile;
+  static constexpr int OFF_Q = OFF_V + kStages * kTile;
+  static constexpr int kQBytes = N * D;              // one term
+  static constexpr int OFF_P = OFF_Q + kQTerms * kQBytes;
+  static constexpr int OFF_BAR = OFF_P + TK * PW;
+  static constexpr int kBars = 2 * kStages + 6;
+  static constexpr int OFF_F4 = OFF_BAR + kBars * 8;  // float4 [NR]: tile max, alpha, beta of the sums
+  static constexpr int OFF_F2 = OFF_F4 + NR * 16;     // float2 [NR]: alpha, beta of O
+  static constexpr int OFF_ROW = OFF_F2 + NR * 8;     // int4 [NR]: lo, hi, position, slope (float)
+  static constexpr int OFF_QS = OFF_ROW + NR * 16;    // float [NR]: 2^e of the query row
+  static constexpr int OFF_RED = OFF_QS + NR * 4;     // float [4][NR]
+  static constexpr int OFF_VMAX = OFF_RED + 4 * NR * 4;  // int [4]
+  static constexpr int OFF_M = OFF_VMAX + 16;         // float [NR]
+  static constexpr int OFF_SCAN = OFF_M + NR * 4;     // int64 [34]
+  static constexpr int OFF_TM = OFF_SCAN + 34 * 8;
+  static constexpr int OFF_ABORT = OFF_TM + 4;
+  static constexpr int SMEM = OFF_ABORT + 4 + 1024;
+  static_assert(kBars % 2 == 0 && OFF_F4 % 16 == 0 && OFF_F2 % 8 == 0 && OFF_ROW % 16 == 0 && OFF_SCAN % 8 == 0, "alignment");
+  static_assert(OFF_Q % 1024 == 0 && OFF_P % 1024 == 0 && kQBytes % 1024 == 0, "swizzle atoms");
+  static_assert(kPerSm * (SMEM + 1024) <= 228 * 1024, "resident CTAs");
+  static_assert(kPTerms * N <= PW, "a key's weights");
+};
+
+template <int D, int NR>
+__global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
+    paged_few_kernel(const PagedLaunch a, const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_v, const WaitTest test) {
+  using C = FewCfg<D, NR>;
+  constexpr int TK = C::TK, N = C::N, PW = C::PW, NS = C::kStages;
+  grid_dep_wait();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);  // a stage's K and V have landed
+  uint64_t* empty = full + NS;                                    // its P V is done
+  uint64_t* s_full = empty + NS;                                  // [2]
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 1;
+  uint64_t* q_full = o_full + 1;
+  uint64_t* drain = q_full + 1;
+  float4* f4_s = reinterpret_cast<float4*>(sm + C::OFF_F4);
+  float2* f2_s = reinterpret_cast<float2*>(sm + C::OFF_F2);
+  int4* row_s = reinterpret_cast<int4*>(sm + C::OFF_ROW);
+  float* qs_s = reinterpret_cast<float*>(sm + C::OFF_QS);
+  float* red_s = reinterpret_cast<float*>(sm + C::OFF_RED);
+  int* vmax_s = reinterpret_cast<int*>(sm + C::OFF_VMAX);
+  float* m_s = reinterpret_cast<float*>(sm + C::OFF_M);
+  uint32_t* tm_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_TM);
+  volatile int* abort = reinterpret_cast<volatile int*>(sm + C::OFF_ABORT);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const Waits wait{a.status, test.limit_ns, abort};
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1);
+    mbar_init(p_full, 4);
+    mbar_init(o_full, 1);
+    mbar_init(q_full, 4);
+    mbar_init(drain, 1);
+    *abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 5) tmem_alloc(tm_slot, C::kCols);
+  PagedShare share;
+  const PagedStart st = paged_start<NR, TK>(a, &share, reinterpret_cast<int64_t*>(sm + C::OFF_SCAN));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tm_slot, tmem_o = tmem + 2 * N;
+  PagedWalk<NR, TK> w(a, st, share);
+  int n = 0;  // tiles so far
+
+  if (warp == 4) {
+    // ------------------------------------------------------------- copies
+    constexpr int kMaxPages = TK / 16;
+    const int per = TK >> a.page_log2;  // pages of a tile
+    const uint32_t page_bytes = (uint32_t)a.page * D;
+    bool go = true;
+    while (go && w.next()) {
+      const PieceKeys<NR, TK> keys(a, w);
+      const int32_t* table = a.table + (int64_t)w.p_b * a.max_blocks;
+      // lane i < per: the tile's page i, loaded a tile ahead; -1: not copied
+      auto page_of = [&](int t) -> int32_t {
+        const int j = t * TK + lane * a.page;
+        if (lane >= per || t >= w.p_t1 || j >= keys.hi || j + a.page <= keys.lo) return -1;
+        const int32_t pg = table[j >> a.page_log2];
+        if (pg >= 0 && pg < a.n_pages) return pg;
+        if (a.status) atomicOr(a.status, LCSC_DEV_BAD_INDEX);
+        return -1;
+      };
+      int32_t next = page_of(keys.t0);
+      for (int t = keys.t0; t < w.p_t1; ++t, ++n) {
+        const int32_t pg = next;
+        next = page_of(t + 1);
+        const int s = n % NS;
+        if (n >= NS && !wait(&empty[s], (uint32_t)(n / NS - 1) & 1u)) {
+          go = false;
+          break;
+        }
+        const uint32_t some = __ballot_sync(0xffffffffu, pg >= 0);
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], 2 * page_bytes * __popc(some));
+        __syncwarp();
+        if (pg >= 0) {
+          const int32_t row = (int32_t)(((int64_t)pg * a.Hkv + w.p_h) << a.page_log2);
+          tma_load_2d(sm + C::OFF_K + s * C::kTile + lane * page_bytes, &map_k, 0, row, &full[s]);
+          tma_load_2d(sm + C::OFF_V + s * C::kTile + lane * page_bytes, &map_v, 0, row, &full[s]);
+        }
+        __syncwarp();
+      }
+    }
+    static_assert(kMaxPages <= 32, "a lane per page");
+    if (*abort) {  // the copies in flight land before the CTA can end
+      for (int i = n > NS ? n - NS : 0; i < n; ++i) mbar_wait(&full[i % NS], (uint32_t)(i / NS) & 1u, a.status, kDrainLimitNs);
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    // ---------------------------------------------------------------- MMA
+    const uint32_t idesc_qk = idesc_dense(0, 0, 128, N);
+    const uint32_t idesc_pv = idesc_dense(0, 0, D, N, true, true);
+    const uint32_t qa = smem_u32(sm + C::OFF_Q), pa = smem_u32(sm + C::OFF_P);
+    bool go = !test.stall || wait(drain, 0);  // a test of the failure path: nothing has committed to it yet
+    bool pend = false;
+    int pieces = 0;
+    auto issue_pv = [&](int m) -> bool {
+      if (!wait(p_full, (uint32_t)m & 1u)) return false;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t va = smem_u32(sm + C::OFF_V + (m % NS) * C::kTile);
+#pragma unroll
+        for (int k = 0; k < TK / 32; ++k)
+#pragma unroll
+          for (int term = 0; term < kPTerms; ++term)
+            mma_ss<1>(tmem_o, smem_desc(va + k * 32 * D, 16, 8 * D, kSwOf<D>),
+                      smem_desc(pa + k * 32 * PW + term * N, 16, 8 * PW, kSwOf<PW>), idesc_pv, k > 0 || term > 0);
+        tc_commit(o_full);
+        tc_commit(&empty[m % NS]);
+      }
+      __syncwarp();
+      return true;
+    };
+    while (go && w.next()) {
+      const PieceKeys<NR, TK> keys(a, w);
+      if (keys.t0 >= w.p_t1) continue;
+      // the softmax warps lay out this piece's queries after the last piece's end
+      if (pend && !(go = issue_pv(n - 1))) break;
+      pend = false;
+      if (!(go = wait(q_full, (uint32_t)pieces & 1u))) break;
+      ++pieces;
+      for (int t = keys.t0; t < w.p_t1; ++t) {
+        const int s = n % NS;
+        if (!(go = wait(&full[s], (uint32_t)(n / NS) & 1u))) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t ka = smem_u32(sm + C::OFF_K + s * C::kTile);
+#pragma unroll
+          for (int term = 0; term < kQTerms; ++term)
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+              mma_ss<1>(tmem + (n & 1) * N, smem_desc(ka + k * 32, 16, 8 * D, kSwOf<D>),
+                        smem_desc(qa + term * C::kQBytes + k * 32, 16, 8 * D, kSwOf<D>), idesc_qk, k > 0 || term > 0);
+          tc_commit(&s_full[n & 1]);
+        }
+        __syncwarp();
+        if (pend && !(go = issue_pv(n - 1))) break;
+        pend = true;
+        ++n;
+      }
+    }
+    if (go && pend) issue_pv(n - 1);
+    if (lane == 0) {  // every MMA has completed before TMEM is freed
+      tc_commit(drain);
+      mbar_wait(drain, 0, a.status, kDrainLimitNs);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax
+    const float c2 = a.sm_scale * kPagedLog2e, cap2 = a.cap * kPagedLog2e;
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    const bool has_dim = D == 128 || lane < 16;
+    const int dim = D == 128 ? tid : warp * 16 + (lane & 15);  // M = 64 accumulators lie in lanes 0-15
+    bool ok = true, first = true;
+    while (ok && w.next()) {
+      if (tid == 0 && first) w.write_meta(false);
+      first = false;
+      const PieceKeys<NR, TK> keys(a, w);
+      const int rows = w.rows(), r0 = w.p_mt * NR;
+      const bool work = keys.t0 < w.p_t1;
+      named_sync(1, 128);  // the last piece is done with shared memory
+      if (tid < NR) {
+        int4 r = make_int4(0, 0, 0, 0);
+        if (tid < rows) {
+          const int i = (r0 + tid) / a.G;
+          paged_span(a, w.p_s, paged_prefix(a, w.p_b), i, &r.x, &r.y);
+          r.z = w.p_s.L - w.p_s.n + i;
+          if (a.docs) r.x = max(r.x, a.docs[w.p_s.q0 + i]);
+          if (a.slopes) r.w = __float_as_int(a.slopes[w.p_h * a.G + (r0 + tid) % a.G] * kPagedLog2e);
+        }
+        row_s[tid] = r;
+      }
+      if (work) {
+        // the query's terms, a warp per row
+        for (int r = warp; r < N; r += 4) {
+          constexpr int VPL = D / 32;
+          float v[VPL];
+#pragma unroll
+          for (int i = 0; i < VPL; ++i) v[i] = 0.f;
+          if (r < rows) {
+            const int row = r0 + r;
+            const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q) + (w.p_s.q0 + row / a.G) * a.q_stride +
+                                (int64_t)(w.p_h * a.G + row % a.G) * D + lane * VPL;
+            if constexpr (VPL == 4) {
+              const uint2 u = *reinterpret_cast<const uint2*>(p);
+              v[0] = bf16_val((uint16_t)u.x), v[1] = bf16_val((uint16_t)(u.x >> 16));
+              v[2] = bf16_val((uint16_t)u.y), v[3] = bf16_val((uint16_t)(u.y >> 16));
+            } else {
+              const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+              v[0] = bf16_val((uint16_t)u), v[1] = bf16_val((uint16_t)(u >> 16));
+            }
+          }
+          float amax = 0.f;
+#pragma unroll
+          for (int i = 0; i < VPL; ++i) amax = fmaxf(amax, fabsf(v[i]));
+          amax = warp_max(amax);
+          const int ex = amax > 0.f ? (int)(__float_as_uint(amax) >> 23) - 127 - 7 : 0;
+          const float f = pow2(-ex);
+          uint16_t hi[VPL / 2], lo[VPL / 2];
+#pragma unroll
+          for (int i = 0; i < VPL / 2; ++i) {
+            const float x = v[2 * i] * f, y = v[2 * i + 1] * f;
+            hi[i] = e4m3x2_code(x, y);
+            const float2 h = e4m3x2_val(hi[i]);
+            lo[i] = e4m3x2_code(x - h.x, y - h.y);
+          }
+          uint8_t* q = sm + C::OFF_Q + swz<D>(r, lane * VPL);
+          if constexpr (VPL == 4) {
+            *reinterpret_cast<uint32_t*>(q) = hi[0] | ((uint32_t)hi[1] << 16);
+            *reinterpret_cast<uint32_t*>(q + C::kQBytes) = lo[0] | ((uint32_t)lo[1] << 16);
+          } else {
+            *reinterpret_cast<uint16_t*>(q) = hi[0];
+            *reinterpret_cast<uint16_t*>(q + C::kQBytes) = lo[0];
+          }
+          // a query that is not finite gives scores that are not numbers
+          if (lane == 0 && r < NR) qs_s[r] = amax <= 3.402823466e38f ? pow2(ex) : NAN;
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+      }
+      named_sync(1, 128);  // row_s and qs_s
+      int lo_max = 0, hi_min = INT_MAX;
+      for (int r = 0; r < rows; ++r) lo_max = max(lo_max, row_s[r].x), hi_min = min(hi_min, row_s[r].y);
+      const bool one_span = lo_max <= keys.lo && hi_min >= keys.hi;
+
+      float l[NR], o[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) l[r] = 0.f, o[r] = 0.f;
+      float m_run = -INFINITY;  // thread r < NR: running max of row r
+      const int32_t* table = a.table + (int64_t)w.p_b * a.max_blocks;
+      // this thread's key of a tile: its page two tiles ahead, its scales one
+      auto page_of = [&](int t) -> int64_t {
+        const int j = t * TK + tid;
+        if (t >= w.p_t1 || j >= keys.hi || (j | (a.page - 1)) < keys.lo) return -1;
+        const int32_t pg = table[j >> a.page_log2];
+        return pg >= 0 && pg < a.n_pages ? (int64_t)pg * a.Hkv + w.p_h : -1;
+      };
+      int64_t ph = page_of(keys.t0), ph_next = page_of(keys.t0 + 1);
+      float ks = ph < 0 ? -1.f : a.k_scale[ph], vs = ph < 0 ? 0.f : a.v_scale[ph];
+      auto add_o = [&](int m) -> bool {  // O of tile m into the running one
+        if (!wait(o_full, (uint32_t)m & 1u)) return false;
+        tc_fence_after();
+        uint32_t x[NR];
+        tmem_ld(tmem_o + lane_base, x);
+        tmem_ld_done(x);
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const float2 f = f2_s[r];
+          o[r] = fmaf(o[r], f.x, __uint_as_float(x[r]) * f.y);
+        }
+        return true;
+      };
+      for (int t = keys.t0; t < w.p_t1; ++t, ++n) {
+        const float ks_next = ph_next < 0 ? -1.f : a.k_scale[ph_next], vs_next = ph_next < 0 ? 0.f : a.v_scale[ph_next];
+        ph_next = page_of(t + 2);
+        const int j = t * TK + tid;
+        const bool there = ks >= 0.f && j < keys.hi;  // copied, and of this request
+        const bool seen = there && j >= keys.lo;
+        const float kf = ks * c2;
+        float s[NR];
+        ok = wait(&s_full[n & 1], (uint32_t)(n >> 1) & 1u);
+        if (ok) {
+          tc_fence_after();
+          uint32_t x[NR];
+          tmem_ld(tmem + (n & 1) * N + lane_base, x);
+          tmem_ld_done(x);
+          float mine = -INFINITY;
+          const bool inside = one_span || (t * TK >= lo_max && (t + 1) * TK <= hi_min);
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            float y = __uint_as_float(x[r]) * (kf * qs_s[r]);
+            if (a.cap > 0.f) y = paged_cap(y, cap2);
+            if (a.slopes) y -= __int_as_float(row_s[r].w) * (float)abs(row_s[r].z - j);
+            bool see = seen;
+            if (!inside) see = see && j >= row_s[r].x && j < row_s[r].y;
+            s[r] = see ? y : -INFINITY;
+            const float top = warp_redux_max(s[r]);
+            if (lane == r) mine = top;
+          }
+          if (lane < NR) red_s[warp * NR + lane] = mine;
+          const int vm = __reduce_max_sync(0xffffffffu, there ? __float_as_int(vs) : 0);
+          if (lane == 0) vmax_s[warp] = vm;
+        }
+        if (!(ok = named_and(1, 128, ok))) break;
+        const float vmax = __int_as_float(max(max(vmax_s[0], vmax_s[1]), max(vmax_s[2], vmax_s[3])));
+        float al = 0.f, be = 0.f, mt = -INFINITY;
+        if (tid < NR) {
+          mt = fmaxf(fmaxf(red_s[tid], red_s[NR + tid]), fmaxf(red_s[2 * NR + tid], red_s[3 * NR + tid]));
+          const float m_new = fmaxf(m_run, mt), ref = m_new == -INFINITY ? 0.f : m_new;
+          al = paged_ex2(m_run - ref);
+          be = paged_ex2(mt - ref);
+          m_run = m_new;
+          f4_s[tid] = make_float4(mt == -INFINITY ? 0.f : mt, al, be, 0.f);
+        }
+        // the last tile's O before its factors give way to this tile's
+        const bool o_in = t == keys.t0 || add_o(n - 1);
+        if (!(ok = named_and(1, 128, o_in))) break;
+        if (tid < NR) f2_s[tid] = make_float2(al, be * vmax * (1.f / 256.f));
+        // weights in [0, 256], relative to the tile's maxima and largest V scale
+        const float vr = there && vmax > 0.f ? __fdividef(vs, vmax) * 256.f : 0.f;
+        uint8_t* prow = sm + C::OFF_P;
+#pragma unroll
+        for (int r8 = 0; r8 < N; r8 += 16) {
+          uint32_t code[kPTerms][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int term = 0; term < kPTerms; ++term) code[term][i] = 0;
+            if (r8 + 4 * i < NR) {
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const int r = r8 + 4 * i + 2 * half;
+                const float4 fa = f4_s[r], fb = f4_s[r + 1];
+                const float pa = paged_ex2(s[r] - fa.x), pb = paged_ex2(s[r + 1] - fb.x);
+                l[r] = fmaf(l[r], fa.y, pa * fa.z);
+                l[r + 1] = fmaf(l[r + 1], fb.y, pb * fb.z);
+                __half2 x = __floats2half2_rn(pa * vr, pb * vr);
+#pragma unroll
+                for (int term = 0; term < kPTerms; ++term) {
+                  const uint32_t c8 = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(x), __NV_SATFINITE, __NV_E4M3);
+                  code[term][i] |= c8 << (16 * half);
+                  if (term + 1 < kPTerms) x = __hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c8, __NV_E4M3)));
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int term = 0; term < kPTerms; ++term)
+            *reinterpret_cast<uint4*>(prow + swz<PW>(tid, term * N + r8)) =
+                make_uint4(code[term][0], code[term][1], code[term][2], code[term][3]);
+        }
+        if (!there) {  // no such key: its V row may hold anything, and 0 x NaN is NaN
+          uint4* v = reinterpret_cast<uint4*>(sm + C::OFF_V + (n % NS) * C::kTile + tid * D);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) v[i] = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+        ks = ks_next, vs = vs_next;
+      }
+      if (ok && work) {
+        named_sync(1, 128);  // f2_s of the last tile
+        ok = add_o(n - 1);
+      }
+      float mine = 0.f;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const float sum = warp_sum(l[r]);
+        if (lane == r) mine = sum;
+      }
+      if (lane < NR) red_s[warp * NR + lane] = mine;
+      if (tid < NR) m_s[tid] = m_run;
+      if (!(ok = named_and(1, 128, ok))) break;
+      if (w.whole()) {
+        if (has_dim) {
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+            if (r < rows)
+              paged_write<D>(a, w.p_s, w.p_h, r0 + r, dim, o[r], m_s[r],
+                             red_s[r] + red_s[NR + r] + red_s[2 * NR + r] + red_s[3 * NR + r]);
+        }
+      } else {
+        const int64_t at = w.slot() * NR;
+        if (has_dim) {
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+            if (r < rows) a.part_o[(at + r) * D + dim] = o[r];
+        }
+        if (tid < rows) {
+          a.part_ml[(at + tid) * 2] = m_s[tid];
+          a.part_ml[(at + tid) * 2 + 1] = red_s[tid] + red_s[NR + tid] + red_s[2 * NR + tid] + red_s[3 * NR + tid];
+        }
+      }
+    }
+    if (first && tid == 0) w.write_meta(true);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 5) tmem_dealloc(tmem, C::kCols);
+}
+
+// ---------------------------------------------------------------- host side
+
+PFN_cuTensorMapEncodeTiled_v12000 tiled_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+// The pool's codes as rows of D bytes; a box is `rows` of them (16-byte aligned
+// base, D a multiple of 16, every copy from column 0).
+bool map_pool(CUtensorMap* m, const PagedLaunch& a, const void* base, int rows) {
+  auto fn = tiled_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)a.D, (cuuint64_t)a.n_pages * a.Hkv * a.page};
+  cuuint64_t strides[1] = {(cuuint64_t)a.D};
+  cuuint32_t box[2] = {(cuuint32_t)a.D, (cuuint32_t)rows};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, a.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NR>
+cudaError_t launch_few(const PagedLaunch& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
+  using C = FewCfg<D, NR>;
+  auto kern = paged_few_kernel<D, NR>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(a.ctas), dim3(kFewThreads), C::SMEM, stream, a, k, v, wait_test());
+}
+
+template <int D>
+cudaError_t launch_mma(const PagedLaunch& a, const PagedForm& f, const CUtensorMap& k, const CUtensorMap& v,
+                       cudaStream_t stream) {
+  switch (f.rows) {
+    case 8: return launch_few<D, 8>(a, k, v, stream);
+    case 16: return launch_few<D, 16>(a, k, v, stream);
+    default: return launch_few<D, 32>(a, k, v, stream);
+  }
+}
+
+}  // namespace
+
+PagedForm paged_mma_form(int D, int G, int64_t max_new) {
+  const int64_t rows = max_new * G;
+  return {1, rows <= 8 ? 8 : rows <= 16 ? 16 : 32, 2 * sm_count()};
+}
+
+cudaError_t launch_paged_mma(const PagedLaunch& a, const PagedForm& f, cudaStream_t stream) {
+  CUtensorMap k, v;
+  if (!map_pool(&k, a, a.k, a.page) || !map_pool(&v, a, a.v, a.page)) return cudaErrorInvalidValue;
+  return a.D == 128 ? launch_mma<128>(a, f, k, v, stream) : launch_mma<64>(a, f, k, v, stream);
+}
+
+}  // namespace lcsc

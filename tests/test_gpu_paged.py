@@ -431,3 +431,20 @@ def test_serving_steps(cuda_lib, dtype):
         # one rounding of the output, and the weights' and scores' errors of the attention tests' bound
         assert (err <= np.abs(ref[:live]) * eps + (2.0 ** -10 if td == BF16 else 2.0 ** -16) * vmax[:live, :, None]).all()
         cached = np.where(n_new < 0, 0, cached + np.maximum(n_new, 0))
+
+
+# ------------------------------------------------------------ failure path
+
+@pytest.mark.parametrize("new", [[1, 1], [1, 30], [90, 60]])
+def test_wait_runs_out_then_recovers(cuda_lib, new):
+    """A bounded wait of the tensor-core forms that runs out (only that: every
+    CTA ends by itself) is reported, and the next call is right."""
+    c = Case([3000, 400], new, 8, 2, 128, 64, BF16, seed=20)
+    L.set_wait_test(20_000_000, True)
+    try:
+        c.run()
+        torch.cuda.synchronize()
+        assert c.status.item() == L.DEV_TIMEOUT
+    finally:
+        L.set_wait_test(0, False)
+    c.run().check()
