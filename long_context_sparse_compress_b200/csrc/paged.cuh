@@ -81,7 +81,7 @@ cudaError_t launch_paged_store(const PagedStoreLaunch& a, cudaStream_t stream);
 // The form of the attention kernel that serves a call (from the host's
 // arguments alone), its rows per item and the CTAs it launches.
 struct PagedForm {
-  int kind;  // 0: float32 on the CUDA cores, 1: few rows on the tensor cores
+  int kind;  // 0: float32 on the CUDA cores, 1: few rows on the tensor cores, 2: many
   int rows;
   int ctas;
 };

@@ -29,6 +29,14 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
 }
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld_32(taddr, r); }
 
+// Store counterpart of tmem_ld_32.
+__device__ __forceinline__ void tmem_st_32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]));
+}
+
 // Waits for this thread's tcgen05.ld with the registers passed through, so
 // that no use of them moves before the wait.
 template <int N>
@@ -552,6 +560,599 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
   if (warp == 5) tmem_dealloc(tmem, C::kCols);
 }
 
+// ============================================================== many rows
+// Prompts: blocks of 256 query rows, as two tiles of 128 that share K and V.
+//   S [128 rows][128 keys] = Q K^T     Q: two E4M3 terms, K as stored (kind::f8f6f4)
+//   O [128 rows][D dims]  += P V       P and V in f16 (kind::f16)
+// A softmax warpgroup owns a tile and a thread one row of it: maxima and sums
+// need no exchange.  O stays in TMEM; it is rescaled only when a row's maximum
+// has grown by more than 2^8 over the reference (weights then reach 256, well
+// inside f16).  V's codes become f16 numbers exactly: four warps read them
+// from global memory a tile ahead and write code * 2^7 * (page scale / largest
+// page scale of the piece), which is exact for scales down to 2^-13 of the
+// largest and loses only what lies below 2^-31 of the largest possible |V|.  Two
+// tiles keep the tensor cores busy with one while the other's weights are made.
+//
+// Bound: per 256 x 128 step the products take 2,048 cycles, as do the
+// exponentials (32 K at 16 a cycle), and shared memory about 2,900 (operands
+// 2,048, P 512, V 256, K 128).
+
+constexpr int kManyThreads = 448;  // warps 0-7 softmax (two tiles), 8-11 V, 12 copies, 13 MMA
+constexpr int kManyRows = 256;
+constexpr float kLazy = 8.f;       // growth of a row's maximum (base-2 units) that rescales O
+
+template <int D>
+struct ManyCfg {
+  static constexpr int TK = 128;
+  static constexpr int kQTerm = 128 * D;              // one term of a tile's queries
+  static constexpr int kK = TK * D;
+  static constexpr int kV = TK * D * 2;
+  static constexpr int kP = 128 * TK * 2;
+  static constexpr int OFF_Q = 0;                     // [2 tiles][2 terms]
+  static constexpr int OFF_K = OFF_Q + 4 * kQTerm;    // [2]
+  static constexpr int OFF_V = OFF_K + 2 * kK;        // [2]
+  static constexpr int OFF_P = OFF_V + 2 * kV;        // [2 tiles]
+  static constexpr int OFF_BAR = OFF_P + 2 * kP;
+  static constexpr int kBars = 18;
+  static constexpr int OFF_SCAN = OFF_BAR + kBars * 8;  // int64 [34]
+  static constexpr int OFF_VREF = OFF_SCAN + 34 * 8;    // int: largest V scale of the piece (bits)
+  static constexpr int OFF_TM = OFF_VREF + 4;
+  static constexpr int OFF_ABORT = OFF_TM + 4;
+  static constexpr int SMEM = OFF_ABORT + 4 + 1024;
+  static_assert(OFF_K % 1024 == 0 && OFF_V % 1024 == 0 && OFF_P % 1024 == 0 && OFF_SCAN % 8 == 0, "alignment");
+  static_assert(SMEM <= 232448 - 64, "shared memory per block");
+};
+
+// One row's scores: factors, mask and bias of the thread's query row.
+struct ManyRow {
+  int lo, hi, pos;
+  float rf, slope;  // sm_scale log2(e) 2^e of the query; bias per position in base-2 units
+};
+
+// 16 raw products of the keys j .. j + 15 (page scale ks; < 0: not there) to scores in base-2 units.
+__device__ __forceinline__ void many_scores(const PagedLaunch& a, const ManyRow& r, float cap2, float ks, int j,
+                                            bool inside, const uint32_t* x, float* y) {
+  const float c = ks * r.rf;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float v = __uint_as_float(x[i]) * c;
+    if (a.cap > 0.f) v = paged_cap(v, cap2);
+    if (a.slopes) v -= r.slope * (float)abs(r.pos - (j + i));
+    if (!inside && !(ks >= 0.f && j + i >= r.lo && j + i < r.hi)) v = -INFINITY;
+    y[i] = v;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kManyThreads, 1)
+    paged_many_kernel(const PagedLaunch a, const __grid_constant__ CUtensorMap map_k, const WaitTest test) {
+  using C = ManyCfg<D>;
+  constexpr int TK = C::TK, M = kManyRows;
+  grid_dep_wait();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);  // [2]
+  uint64_t* k_empty = k_full + 2;    // [2] both tiles' Q K^T are done
+  uint64_t* v_full = k_full + 4;     // [2] V is there in f16
+  uint64_t* v_empty = k_full + 6;    // [2] both tiles' P V are done
+  uint64_t* s_full = k_full + 8;     // [2 tiles]
+  uint64_t* p_full = k_full + 10;    // [2 tiles] P is written, S is read
+  uint64_t* pv_done = k_full + 12;   // [2 tiles]
+  uint64_t* q_full = k_full + 14;    // both tiles' queries
+  uint64_t* ref_full = k_full + 15;  // the piece's largest V scale
+  uint64_t* piece_done = k_full + 16;
+  uint64_t* drain = k_full + 17;
+  volatile int* vref_s = reinterpret_cast<volatile int*>(sm + C::OFF_VREF);
+  uint32_t* tm_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_TM);
+  volatile int* abort = reinterpret_cast<volatile int*>(sm + C::OFF_ABORT);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const Waits wait{a.status, test.limit_ns, abort};
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 4), mbar_init(&v_empty[i], 1);
+      mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4), mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(q_full, 8);
+    mbar_init(ref_full, 4);
+    mbar_init(piece_done, 8);
+    mbar_init(drain, 1);
+    *abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 13) tmem_alloc(tm_slot, 512);
+  PagedShare share;
+  const PagedStart st = paged_start<M, TK>(a, &share, reinterpret_cast<int64_t*>(sm + C::OFF_SCAN));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tm_slot;  // S of tile 0, 1 (128 columns each), O of tile 0, 1
+  PagedWalk<M, TK> w(a, st, share);
+
+  if (warp == 12) {
+    // ------------------------------------------------------------- copies
+    const int per = TK >> a.page_log2;
+    const uint32_t page_bytes = (uint32_t)a.page * D;
+    int n = 0;
+    bool go = true;
+    while (go && w.next()) {
+      const PieceKeys<M, TK> keys(a, w);
+      const int32_t* table = a.table + (int64_t)w.p_b * a.max_blocks;
+      auto page_of = [&](int t) -> int32_t {
+        const int j = t * TK + lane * a.page;
+        if (lane >= per || t >= w.p_t1 || j >= keys.hi || j + a.page <= keys.lo) return -1;
+        const int32_t pg = table[j >> a.page_log2];
+        if (pg >= 0 && pg < a.n_pages) return pg;
+        if (a.status) atomicOr(a.status, LCSC_DEV_BAD_INDEX);
+        return -1;
+      };
+      int32_t next = page_of(keys.t0);
+      for (int t = keys.t0; t < w.p_t1; ++t, ++n) {
+        const int32_t pg = next;
+        next = page_of(t + 1);
+        const int s = n & 1;
+        if (n >= 2 && !wait(&k_empty[s], (uint32_t)((n >> 1) - 1) & 1u)) {
+          go = false;
+          break;
+        }
+        const uint32_t some = __ballot_sync(0xffffffffu, pg >= 0);
+        if (lane == 0) mbar_arrive_expect_tx(&k_full[s], page_bytes * __popc(some));
+        __syncwarp();
+        if (pg >= 0)
+          tma_load_2d(sm + C::OFF_K + s * C::kK + lane * page_bytes, &map_k, 0,
+                      (int32_t)(((int64_t)pg * a.Hkv + w.p_h) << a.page_log2), &k_full[s]);
+        __syncwarp();
+      }
+    }
+    if (*abort)
+      for (int i = n > 2 ? n - 2 : 0; i < n; ++i) mbar_wait(&k_full[i & 1], (uint32_t)(i >> 1) & 1u, a.status, kDrainLimitNs);
+    __syncwarp();
+  } else if (warp == 13) {
+    // ---------------------------------------------------------------- MMA
+    const uint32_t idesc_qk = idesc_dense(0, 0, 128, TK);
+    const uint32_t idesc_pv = idesc_dense(0, 0, 128, D, false, true);
+    const uint32_t qa = smem_u32(sm + C::OFF_Q);
+    bool go = !test.stall || wait(drain, 0);  // a test of the failure path: nothing has committed to it yet
+    int n = 0, pieces = 0, cnt[2] = {0, 0};
+    auto issue_pv = [&](int g, bool last, bool acc) {  // P V of tile n - 1 (its P and V are there)
+      if (lane == 0) {
+        const int b = (n - 1) & 1;
+        const uint32_t pa = smem_u32(sm + C::OFF_P + g * C::kP), va = smem_u32(sm + C::OFF_V + b * C::kV);
+#pragma unroll
+        for (int k = 0; k < TK / 16; ++k)
+          mma_ss<0>(tmem + 256 + g * 128, smem_desc(pa + (k / 4) * (128 * 128) + (k % 4) * 32, 16, 1024, kSw128),
+                    smem_desc(va + k * 16 * 128, TK * 128, 1024, kSw128), idesc_pv, acc || k > 0);
+        tc_commit(&pv_done[g]);
+        if (last) tc_commit(&v_empty[b]);
+      }
+      __syncwarp();
+    };
+    while (go && w.next()) {
+      const PieceKeys<M, TK> keys(a, w);
+      if (keys.t0 >= w.p_t1) continue;
+      const int tiles = w.rows() > 128 ? 2 : 1;
+      if (!(go = wait(q_full, (uint32_t)pieces & 1u))) break;
+      ++pieces;
+      for (int t = keys.t0; go && t < w.p_t1; ++t) {
+        const int s = n & 1;
+        if (!(go = wait(&k_full[s], (uint32_t)(n >> 1) & 1u))) break;
+        for (int g = 0; g < tiles; ++g) {
+          if (t > keys.t0 && !(go = wait(&p_full[g], (uint32_t)(cnt[g] - 1) & 1u))) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t ka = smem_u32(sm + C::OFF_K + s * C::kK);
+#pragma unroll
+            for (int term = 0; term < kQTerms; ++term)
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k)
+                mma_ss<1>(tmem + g * 128, smem_desc(qa + (2 * g + term) * C::kQTerm + k * 32, 16, 8 * D, kSwOf<D>),
+                          smem_desc(ka + k * 32, 16, 8 * D, kSwOf<D>), idesc_qk, k > 0 || term > 0);
+            tc_commit(&s_full[g]);
+            if (g == tiles - 1) tc_commit(&k_empty[s]);
+          }
+          __syncwarp();
+          ++cnt[g];
+          if (t > keys.t0) {
+            if (g == 0 && !(go = wait(&v_full[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u))) break;
+            tc_fence_after();
+            issue_pv(g, g == tiles - 1, t - 1 > keys.t0);
+          }
+        }
+        if (go) ++n;
+      }
+      for (int g = 0; go && g < tiles; ++g) {
+        if (!(go = wait(&p_full[g], (uint32_t)(cnt[g] - 1) & 1u))) break;
+        if (g == 0 && !(go = wait(&v_full[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u))) break;
+        tc_fence_after();
+        issue_pv(g, g == tiles - 1, w.p_t1 - 1 > keys.t0);
+      }
+    }
+    if (lane == 0) {
+      tc_commit(drain);
+      mbar_wait(drain, 0, a.status, kDrainLimitNs);
+    }
+    __syncwarp();
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------------ V
+    // Warp v has the keys 32 v .. 32 v + 31 of a tile; 8 (D = 64: 4) lanes
+    // read a row's chunks of 16 codes.
+    constexpr int LPR = D / 16, RPI = 32 / LPR, IT = 32 / RPI;  // lanes per row, rows per step, steps
+    const int v = warp - 8, c = lane % LPR, rsub = lane / LPR;
+    int n = 0, pieces = 0;
+    bool ok = true;
+    while (ok && w.next()) {
+      const PieceKeys<M, TK> keys(a, w);
+      const int32_t* table = a.table + (int64_t)w.p_b * a.max_blocks;
+      if (keys.t0 >= w.p_t1) {
+        // nothing to do, but the piece counts
+        ok = named_and(2, 128, true);
+        if (pieces > 0) ok = named_and(2, 128, wait(piece_done, (uint32_t)(pieces - 1) & 1u));
+        ++pieces;
+        if (ok && lane == 0) mbar_arrive(ref_full);
+        continue;
+      }
+      // (page, head) of a key, or -1
+      auto page_of = [&](int j) -> int64_t {
+        if (j >= keys.hi || (j | (a.page - 1)) < keys.lo) return -1;
+        const int32_t pg = table[j >> a.page_log2];
+        return pg >= 0 && pg < a.n_pages ? (int64_t)pg * a.Hkv + w.p_h : -1;
+      };
+      // the largest scale of the piece's pages
+      int top = 0;
+      for (int j = max(keys.t0 * TK, keys.lo / a.page * a.page) + (tid - 256) * a.page; j < min(keys.hi, w.p_t1 * TK);
+           j += 128 * a.page) {
+        const int64_t ph = page_of(j);
+        if (ph >= 0) top = max(top, __float_as_int(a.v_scale[ph]));
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      // the last piece's softmax has read its scale
+      ok = pieces == 0 || wait(piece_done, (uint32_t)(pieces - 1) & 1u);
+      ++pieces;
+      if (tid == 256) *vref_s = 0;
+      if (!(ok = named_and(2, 128, ok))) break;
+      if (lane == 0) atomicMax(const_cast<int*>(vref_s), top);
+      named_sync(2, 128);
+      const float vref = __int_as_float(*vref_s);
+      if (lane == 0) mbar_arrive(ref_full);
+      const float inv = vref > 0.f ? __fdividef(1.f, vref) * 32768.f : 0.f;
+      uint4 raw[IT];
+      float sc[2];  // scales of the warp's keys 0-15 and 16-31 (0: not there)
+      auto fetch = [&](int t) {
+        if (t >= w.p_t1) return;
+        const int j0 = t * TK + v * 32;
+        const int64_t p0 = page_of(j0), p1 = page_of(j0 + 16);
+        sc[0] = p0 < 0 ? 0.f : a.v_scale[p0];
+        sc[1] = p1 < 0 ? 0.f : a.v_scale[p1];
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          const int r = i * RPI + rsub, j = j0 + r;
+          const int64_t ph = i < IT / 2 ? p0 : p1;
+          raw[i] = make_uint4(0, 0, 0, 0);
+          if (ph >= 0 && j < keys.hi)
+            raw[i] = *reinterpret_cast<const uint4*>(a.v + (ph * a.page + (j & (a.page - 1))) * D + c * 16);
+        }
+      };
+      fetch(keys.t0);
+      for (int t = keys.t0; t < w.p_t1; ++t, ++n) {
+        const int b = n & 1;
+        if (n >= 2 && !(ok = wait(&v_empty[b], (uint32_t)((n >> 1) - 1) & 1u))) break;
+        uint8_t* dst = sm + C::OFF_V + b * C::kV;
+        // codes to f16 (exact), times 2^15 scale / vref / 2^8: the code's bits
+        // as an f16 read 2^-8 of its value, so the factor is 2^15 at most
+        const __half2 f[2] = {__float2half2_rn(sc[0] * inv), __float2half2_rn(sc[1] * inv)};
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          const uint32_t wd[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+          uint32_t h[8];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            // bytes to the high halves of 16-bit lanes, then the exponent and mantissa one bit down
+            const uint32_t u0 = __byte_perm(wd[q], 0, 0x1404), u1 = __byte_perm(wd[q], 0, 0x3424);
+            const uint32_t e0 = (u0 & 0x80008000u) | ((u0 & 0x7f007f00u) >> 1);
+            const uint32_t e1 = (u1 & 0x80008000u) | ((u1 & 0x7f007f00u) >> 1);
+            const __half2 m0 = __hmul2(*reinterpret_cast<const __half2*>(&e0), f[i >= IT / 2]);
+            const __half2 m1 = __hmul2(*reinterpret_cast<const __half2*>(&e1), f[i >= IT / 2]);
+            h[2 * q] = *reinterpret_cast<const uint32_t*>(&m0);
+            h[2 * q + 1] = *reinterpret_cast<const uint32_t*>(&m1);
+          }
+          // 16 dims are two chunks of a 64-dim atom; the lanes of the second
+          // atom store theirs in the other order, so that a store covers all banks
+          const int r = v * 32 + i * RPI + rsub, atom = c / 4, ch = (c % 4) * 2;
+          const bool flip = (c / 4) & 1;
+          uint8_t* at = dst + atom * (TK * 128);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const bool second = (q == 1) != flip;
+            *reinterpret_cast<uint4*>(at + swz<128>(r, (ch + (second ? 1 : 0)) * 16)) =
+                second ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        }
+        fetch(t + 1);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_full[b]);
+      }
+      if (!(ok = named_and(2, 128, ok))) break;  // the four warps go on or stop together
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int g = warp / 4;  // the tile
+    const int row_in = tid % 128;
+    const float cap2 = a.cap * kPagedLog2e;
+    const uint32_t lane_base = (uint32_t)((warp % 4) * 32) << 16;
+    const uint32_t s_addr = tmem + g * 128 + lane_base, o_addr = tmem + 256 + g * 128 + lane_base;
+    bool ok = true, first = true;
+    int cnt = 0, pieces = 0;
+    while (ok && w.next()) {
+      if (tid == 0 && first) w.write_meta(false);
+      first = false;
+      const PieceKeys<M, TK> keys(a, w);
+      const int rows = w.rows(), r0 = w.p_mt * M + g * 128;
+      const bool mine = g * 128 + row_in < rows, tile_live = g * 128 < rows;
+      ManyRow r = {0, INT_MAX, 0, 0.f, 0.f};
+      if (mine) {
+        const int i = (r0 + row_in) / a.G;
+        paged_span(a, w.p_s, paged_prefix(a, w.p_b), i, &r.lo, &r.hi);
+        r.pos = w.p_s.L - w.p_s.n + i;
+        if (a.docs) r.lo = max(r.lo, a.docs[w.p_s.q0 + i]);
+        if (a.slopes) r.slope = a.slopes[w.p_h * a.G + (r0 + row_in) % a.G] * kPagedLog2e;
+      }
+      const bool work = keys.t0 < w.p_t1;
+      if (work) {
+        // the tile's query terms, a warp per row and four rows at a time; a
+        // lane keeps the factor of its own row
+        if (tile_live) {
+          constexpr int VPL = D / 32;
+#pragma unroll 1
+          for (int i4 = 0; i4 < 32; i4 += 4) {
+            uint32_t u[4][VPL / 2];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int ri = (warp % 4) * 32 + i4 + q, row = r0 + ri;
+#pragma unroll
+              for (int i = 0; i < VPL / 2; ++i) u[q][i] = 0;
+              if (g * 128 + ri < rows) {
+                const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q) + (w.p_s.q0 + row / a.G) * a.q_stride +
+                                    (int64_t)(w.p_h * a.G + row % a.G) * D + lane * VPL;
+                if constexpr (VPL == 4) {
+                  const uint2 x = *reinterpret_cast<const uint2*>(p);
+                  u[q][0] = x.x, u[q][1] = x.y;
+                } else {
+                  u[q][0] = *reinterpret_cast<const uint32_t*>(p);
+                }
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int ri = (warp % 4) * 32 + i4 + q;
+              float x[VPL], amax = 0.f;
+#pragma unroll
+              for (int i = 0; i < VPL / 2; ++i) {
+                x[2 * i] = __uint_as_float(u[q][i] << 16);
+                x[2 * i + 1] = __uint_as_float(u[q][i] & 0xffff0000u);
+              }
+#pragma unroll
+              for (int i = 0; i < VPL; ++i) amax = fmaxf(amax, fabsf(x[i]));
+              amax = warp_redux_max(amax);
+              const int ex = amax > 0.f ? (int)(__float_as_uint(amax) >> 23) - 127 - 7 : 0;
+              const float f = pow2(-ex);
+              uint32_t hi = 0, lo = 0;
+#pragma unroll
+              for (int i = 0; i < VPL / 2; ++i) {
+                const float y0 = x[2 * i] * f, y1 = x[2 * i + 1] * f;
+                const uint16_t hc = e4m3x2_code(y0, y1);
+                const float2 h = e4m3x2_val(hc);
+                hi |= (uint32_t)hc << (16 * i);
+                lo |= (uint32_t)e4m3x2_code(y0 - h.x, y1 - h.y) << (16 * i);
+              }
+              uint8_t* at = sm + C::OFF_Q + 2 * g * C::kQTerm + swz<D>(ri, lane * VPL);
+              if constexpr (VPL == 4) {
+                *reinterpret_cast<uint32_t*>(at) = hi;
+                *reinterpret_cast<uint32_t*>(at + C::kQTerm) = lo;
+              } else {
+                *reinterpret_cast<uint16_t*>(at) = (uint16_t)hi;
+                *reinterpret_cast<uint16_t*>(at + C::kQTerm) = (uint16_t)lo;
+              }
+              if (lane == i4 + q)
+                r.rf = a.sm_scale * kPagedLog2e * (amax <= 3.402823466e38f ? pow2(ex) : NAN);
+            }
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+      }
+      if (!(ok = wait(ref_full, (uint32_t)pieces & 1u))) break;
+      ++pieces;
+      const float vref = __int_as_float(*vref_s);
+      float m_ref = -INFINITY, l = 0.f;
+      const int32_t* table = a.table + (int64_t)w.p_b * a.max_blocks;
+      // lane i < 8: the page of the tile's keys 16 i .. 16 i + 15, two tiles
+      // ahead, and its K scale one ahead
+      auto page_of = [&](int t) -> int64_t {
+        const int j = t * TK + lane * 16;
+        if (lane >= 8 || t >= w.p_t1 || j >= keys.hi || (j | (a.page - 1)) < keys.lo) return -1;
+        const int32_t pg = table[j >> a.page_log2];
+        return pg >= 0 && pg < a.n_pages ? (int64_t)pg * a.Hkv + w.p_h : -1;
+      };
+      if (work && tile_live) {
+        int64_t ph = page_of(keys.t0), ph_next = page_of(keys.t0 + 1);
+        float ks = ph < 0 ? -1.f : a.k_scale[ph];
+        uint8_t* prow = sm + C::OFF_P + g * C::kP;
+        for (int t = keys.t0; t < w.p_t1; ++t) {
+          const float ks_next = ph_next < 0 ? -1.f : a.k_scale[ph_next];
+          ph_next = page_of(t + 2);
+          const int j0 = t * TK;
+          const bool inside = __all_sync(0xffffffffu, r.lo <= j0 && r.hi >= j0 + TK && (lane >= 8 || ks >= 0.f));
+          if (!(ok = wait(&s_full[g], (uint32_t)cnt & 1u))) break;
+          tc_fence_after();
+          // the row's maximum over the tile
+          float top = -INFINITY;
+          uint32_t x[2][32];
+          tmem_ld(s_addr, x[0]);
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            tmem_ld_done(x[h & 1]);
+            if (h < 3) tmem_ld(s_addr + (h + 1) * 32, x[(h + 1) & 1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float kg = __shfl_sync(0xffffffffu, ks, 2 * h + e);
+              if (inside && !a.slopes) {
+                float mx = __uint_as_float(x[h & 1][16 * e]);
+#pragma unroll
+                for (int i = 1; i < 16; ++i) mx = fmaxf(mx, __uint_as_float(x[h & 1][16 * e + i]));
+                mx *= kg * r.rf;
+                if (a.cap > 0.f) mx = paged_cap(mx, cap2);
+                top = fmaxf(top, mx);
+              } else {
+                float y[16];
+                many_scores(a, r, cap2, kg, j0 + 32 * h + 16 * e, inside, &x[h & 1][16 * e], y);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) top = fmaxf(top, y[i]);
+              }
+            }
+          }
+          tmem_ld(s_addr, x[0]);
+          const bool fresh = t == keys.t0;
+          float alpha = 1.f;
+          bool grown = false;
+          if (top > m_ref + kLazy || (fresh && top > -INFINITY)) {
+            alpha = paged_ex2(m_ref - top);  // before the first key: 0
+            grown = !fresh;
+            m_ref = top;
+            l *= alpha;
+          }
+          // P and O: the last tile's P V has read and added to them
+          if (!fresh && !(ok = wait(&pv_done[g], (uint32_t)(cnt - 1) & 1u))) {
+            tmem_ld_done(x[0]);
+            break;
+          }
+          if (__any_sync(0xffffffffu, grown)) {
+            tc_fence_after();
+            tmem_ld_done(x[0]);
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+              uint32_t o[32];
+              tmem_ld(o_addr + d, o);
+              tmem_ld_done(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st_32(o_addr + d, o);
+            }
+            tmem_st_wait();
+          }
+          const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            tmem_ld_done(x[h & 1]);
+            if (h < 3) tmem_ld(s_addr + (h + 1) * 32, x[(h + 1) & 1]);
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float kg = __shfl_sync(0xffffffffu, ks, 2 * h + e);
+              float p[16];
+              if (inside && !a.slopes && !(a.cap > 0.f)) {
+                const float c = kg * r.rf;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) p[i] = paged_ex2(fmaf(__uint_as_float(x[h & 1][16 * e + i]), c, -ref));
+              } else {
+                many_scores(a, r, cap2, kg, j0 + 32 * h + 16 * e, inside, &x[h & 1][16 * e], p);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) p[i] = paged_ex2(p[i] - ref);
+              }
+              float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                s0 += p[i];
+                s1 += p[i + 1];
+                const __half2 hp = __floats2half2_rn(p[i], p[i + 1]);
+                pk[8 * e + i / 2] = *reinterpret_cast<const uint32_t*>(&hp);
+              }
+              l += s0 + s1;
+            }
+            uint8_t* at = prow + (h / 2) * (128 * 128);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(at + swz<128>(row_in, (h & 1) * 64 + i * 16)) =
+                  make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+          }
+          fence_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[g]);
+          ++cnt;
+          ks = ks_next;
+        }
+        if (ok) ok = wait(&pv_done[g], (uint32_t)(cnt - 1) & 1u);
+        tc_fence_after();
+      }
+      if (!ok) break;
+      // O (times 2^7 / vref), the row's maximum and sum
+      if (tile_live) {
+        const float unit = vref * (1.f / 128.f);
+        const int row = r0 + row_in;
+        const int head = w.p_h * a.G + row % a.G;
+        const int64_t at = (w.p_s.q0 + row / a.G) * a.Hq + head;
+        const int64_t part = w.slot() * M + g * 128 + row_in;
+        float f = unit;
+        if (w.whole()) {
+          float top = m_ref, den = l;
+          if (mine && a.sink && w.p_s.L > 0) {
+            const float sg = a.sink[head] * kPagedLog2e, m = fmaxf(top, sg);
+            if (m != -INFINITY) {
+              const float e = paged_ex2(top - m);
+              f *= e;
+              den = fmaf(den, e, paged_ex2(sg - m));
+              top = m;
+            }
+          }
+          f = den > 0.f ? f / den : den == 0.f ? 0.f : den;  // a sum that is no number stays one
+          if (mine && a.lse) a.lse[at] = den == 0.f ? -INFINITY : (top + log2f(den)) * kPagedLn2;
+        } else if (mine) {
+          a.part_ml[part * 2] = m_ref;
+          a.part_ml[part * 2 + 1] = l;
+        }
+#pragma unroll 1
+        for (int d = 0; d < D; d += 32) {
+          uint32_t o[32];
+          if (work) {
+            tmem_ld(o_addr + d, o);
+            tmem_ld_done(o);
+          }
+          if (!mine) continue;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(work && f != 0.f ? __uint_as_float(o[i]) * f : 0.f);
+          if (w.whole()) {
+            uint4* out = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + at * D + d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                pk[q] = (uint32_t)bf16_code(__uint_as_float(o[8 * i + 2 * q])) |
+                        ((uint32_t)bf16_code(__uint_as_float(o[8 * i + 2 * q + 1])) << 16);
+              out[i] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+          } else {
+            uint4* out = reinterpret_cast<uint4*>(a.part_o + part * D + d);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) out[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(piece_done);
+    }
+    if (first && tid == 0) w.write_meta(true);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 13) tmem_dealloc(tmem, 512);
+}
+
 // ---------------------------------------------------------------- host side
 
 PFN_cuTensorMapEncodeTiled_v12000 tiled_fn() {
@@ -590,8 +1191,17 @@ cudaError_t launch_few(const PagedLaunch& a, const CUtensorMap& k, const CUtenso
 }
 
 template <int D>
+cudaError_t launch_many(const PagedLaunch& a, const CUtensorMap& k, cudaStream_t stream) {
+  auto kern = paged_many_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ManyCfg<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(a.ctas), dim3(kManyThreads), ManyCfg<D>::SMEM, stream, a, k, wait_test());
+}
+
+template <int D>
 cudaError_t launch_mma(const PagedLaunch& a, const PagedForm& f, const CUtensorMap& k, const CUtensorMap& v,
                        cudaStream_t stream) {
+  if (f.kind == 2) return launch_many<D>(a, k, stream);
   switch (f.rows) {
     case 8: return launch_few<D, 8>(a, k, v, stream);
     case 16: return launch_few<D, 16>(a, k, v, stream);
@@ -603,6 +1213,7 @@ cudaError_t launch_mma(const PagedLaunch& a, const PagedForm& f, const CUtensorM
 
 PagedForm paged_mma_form(int D, int G, int64_t max_new) {
   const int64_t rows = max_new * G;
+  if (rows > 64) return {2, kManyRows, sm_count()};
   return {1, rows <= 8 ? 8 : rows <= 16 ? 16 : 32, 2 * sm_count()};
 }
 
