@@ -956,6 +956,7 @@ int32_t lcsc_paged_attn(const lcsc_paged_params* p, const lcsc_paged_batch* s, c
   L.Hq = p->n_heads;
   L.Hkv = p->n_kv_heads;
   L.G = p->n_heads / p->n_kv_heads;
+  paged_divisor(L.G, &L.g_mul, &L.g_shift);
   L.D = p->head_dim;
   L.page = p->page_size;
   L.page_log2 = log2_of(p->page_size);

@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kStoreWarps * 32) paged_store_kernel(PagedStor
 constexpr int kFmaRows = 8, kFmaKeys = 64, kFmaThreads = 128;
 
 template <int D>
-__global__ void __launch_bounds__(kFmaThreads) paged_fma_kernel(PagedLaunch a) {
+__global__ void __launch_bounds__(kFmaThreads) paged_fma_kernel(const __grid_constant__ PagedLaunch a) {
   grid_dep_wait();
   constexpr int M = kFmaRows, TK = kFmaKeys;
   constexpr int CH = D / 16;               // 16-byte chunks of a row
@@ -428,11 +428,11 @@ __global__ void __launch_bounds__(kFmaThreads) paged_fma_kernel(PagedLaunch a) {
   __shared__ float al_s[M], m_s[M], l_s[M];
   __shared__ float o_s[PARTS > 1 ? D : 1][M];
   __shared__ int lo_s[M], hi_s[M], pos_s[M];
-  __shared__ int64_t scan_s[34];
+  __shared__ PagedScratch scan_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   PagedShare share;
-  const PagedStart st = paged_start<M, TK>(a, &share, scan_s);
+  const PagedStart st = paged_start<M, TK>(a, &share, &scan_s);
   PagedWalk<M, TK> w(a, st, share);
   bool first = true;
   const float c2 = a.sm_scale * kPagedLog2e, cap2 = a.cap * kPagedLog2e;
@@ -441,14 +441,14 @@ __global__ void __launch_bounds__(kFmaThreads) paged_fma_kernel(PagedLaunch a) {
     first = false;
     const int rows = w.rows(), r0 = w.p_mt * M;
     int item_lo, item_hi, x;
-    paged_span(a, w.p_s, paged_prefix(a, w.p_b), r0 / a.G, &item_lo, &x);
-    paged_span(a, w.p_s, paged_prefix(a, w.p_b), (r0 + rows - 1) / a.G, &x, &item_hi);
+    paged_span(a, w.p_s, paged_prefix(a, w.p_b), paged_div(a, r0), &item_lo, &x);
+    paged_span(a, w.p_s, paged_prefix(a, w.p_b), paged_div(a, r0 + rows - 1), &x, &item_hi);
     const int32_t* table = a.table + (int64_t)w.p_b * a.max_blocks;
     __syncthreads();  // the last piece is done with shared memory
     if (tid < M) {
       int lo = 0, hi = 0, pos = 0;
       if (tid < rows) {
-        const int i = (r0 + tid) / a.G;
+        const int i = paged_div(a, r0 + tid);
         paged_span(a, w.p_s, paged_prefix(a, w.p_b), i, &lo, &hi);
         pos = w.p_s.L - w.p_s.n + i;
         if (a.docs) lo = max(lo, a.docs[w.p_s.q0 + i]);
@@ -460,8 +460,8 @@ __global__ void __launch_bounds__(kFmaThreads) paged_fma_kernel(PagedLaunch a) {
       const int r = i / D, d = i % D;
       float v = 0.f;
       if (r < rows) {
-        const int row = r0 + r;
-        v = load_elem(a.q, (w.p_s.q0 + row / a.G) * a.q_stride + (int64_t)(w.p_h * a.G + row % a.G) * D + d, a.q_dtype);
+        const int row = r0 + r, tok = paged_div(a, row);
+        v = load_elem(a.q, (w.p_s.q0 + tok) * a.q_stride + (int64_t)(w.p_h * a.G + row - tok * a.G) * D + d, a.q_dtype);
       }
       q_s[r][d] = v;
     }
@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(kFmaThreads) paged_fma_kernel(PagedLaunch a) {
           float s = acc[r] * ks * c2;
           if (a.cap > 0.f) s = cap2 * tanhf(s / cap2);
           if (a.slopes && g + r < rows)
-            s -= a.slopes[w.p_h * a.G + (r0 + g + r) % a.G] * (float)abs(pos_s[g + r] - j) * kPagedLog2e;
+            s -= a.slopes[w.p_h * a.G + r0 + g + r - paged_div(a, r0 + g + r) * a.G] * (float)abs(pos_s[g + r] - j) * kPagedLog2e;
           s_s[g + r][key] = (ks >= 0.f && j >= lo_s[g + r] && j < hi_s[g + r]) ? s : -INFINITY;
         }
       }

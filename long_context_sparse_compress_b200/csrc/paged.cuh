@@ -25,6 +25,8 @@ struct PagedLaunch {
   int64_t q_stride;  // values from one token's row to the next
   int q_dtype;
   int Hq, Hkv, G, D;
+  uint32_t g_mul;    // x / G = x * g_mul >> g_shift for 0 <= x < 2^31 (paged_divisor)
+  int g_shift;
   int page, page_log2;
   uint8_t* k;
   uint8_t* v;
@@ -91,7 +93,22 @@ cudaError_t launch_paged_attn(const PagedLaunch& a, const PagedForm& f, cudaStre
 PagedForm paged_mma_form(int D, int G, int64_t max_new);
 cudaError_t launch_paged_mma(const PagedLaunch& a, const PagedForm& f, cudaStream_t stream);
 
+// Multiplier and shift of a division by d >= 1: with 2^(l-1) < d <= 2^l,
+// m = floor(2^(31+l) / d) + 1 = (2^(31+l) + e) / d, 0 < e <= d <= 2^l, so that
+// x m / 2^(31+l) = x / d + x e / (d 2^(31+l)) and the excess is below 1 / d for
+// x < 2^31.  m < 2^32 for d > 1; d = 1 takes m = 2^31, shift 31.
+inline void paged_divisor(int d, uint32_t* mul, int* shift) {
+  int l = 0;
+  while ((1 << l) < d) ++l;
+  *shift = 31 + l;
+  *mul = d == (1 << l) ? 1u << 31 : (uint32_t)(((uint64_t)1 << (31 + l)) / d + 1);
+}
+
 #ifdef __CUDACC__
+
+__device__ __forceinline__ int paged_div(const PagedLaunch& a, int x) {
+  return (int)(((uint64_t)(uint32_t)x * a.g_mul) >> a.g_shift);
+}
 
 constexpr float kPagedLog2e = 1.4426950408889634f;
 constexpr float kPagedLn2 = 0.6931471805599453f;
@@ -143,34 +160,57 @@ __device__ __forceinline__ void paged_tiles(const PagedLaunch& a, const PagedSeq
                                             int* t1) {
   const int rows = s.n * a.G;
   int lo, hi, x;
-  paged_span(a, s, prefix, mt * M / a.G, &lo, &x);
-  paged_span(a, s, prefix, (min(rows, (mt + 1) * M) - 1) / a.G, &x, &hi);
+  paged_span(a, s, prefix, paged_div(a, mt * M), &lo, &x);
+  paged_span(a, s, prefix, paged_div(a, min(rows, (mt + 1) * M) - 1), &x, &hi);
   *t0 = lo / TK;
   *t1 = max(*t0 + 1, (hi + TK - 1) / TK);
 }
 
-// Units of one request and head.
 template <int M, int TK>
-__device__ __forceinline__ int64_t paged_units(const PagedLaunch& a, int b) {
+__device__ __forceinline__ int paged_tile_count(const PagedLaunch& a, const PagedSeq& s, int prefix, int mt) {
+  if ((int64_t)mt * M >= (int64_t)s.n * a.G) return 0;
+  int t0, t1;
+  paged_tiles<M, TK>(a, s, prefix, mt, &t0, &t1);
+  return t1 - t0;
+}
+
+__device__ __forceinline__ int64_t paged_warp_sum(int64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Units of a request's head, by a whole warp (the same request in every lane).
+template <int M, int TK>
+__device__ __forceinline__ int64_t paged_units_warp(const PagedLaunch& a, int b) {
   const PagedSeq s = paged_seq(a, b);
   const int prefix = paged_prefix(a, b);
   int64_t u = 0;
-  for (int mt = 0; mt * M < s.n * a.G; ++mt) {
-    int t0, t1;
-    paged_tiles<M, TK>(a, s, prefix, mt, &t0, &t1);
-    u += t1 - t0;
-  }
-  return u;
+  for (int mt = threadIdx.x & 31; (int64_t)mt * M < (int64_t)s.n * a.G; mt += 32)
+    u += paged_tile_count<M, TK>(a, s, prefix, mt);
+  return paged_warp_sum(u);
 }
 
-// Where a CTA's share begins, found once by the whole CTA.
-struct PagedStart {
-  int64_t total;  // units of the call
-  int64_t first;  // of the request the share begins in
-  int b;
-};
+// Units of request b, one request per lane (a.B: none): those of few row
+// blocks by their lane, the others by the warp together.
+template <int M, int TK>
+__device__ __forceinline__ int64_t paged_units(const PagedLaunch& a, int b) {
+  PagedSeq s = {0, 0, 0};
+  if (b < a.B) s = paged_seq(a, b);
+  const int prefix = b < a.B ? paged_prefix(a, b) : 0;
+  const bool few = (int64_t)s.n * a.G <= 4 * M;
+  int64_t u = 0;
+  if (few)
+    for (int mt = 0; mt < 4; ++mt) u += paged_tile_count<M, TK>(a, s, prefix, mt);
+  for (unsigned todo = __ballot_sync(0xffffffffu, !few); todo; todo &= todo - 1) {
+    const int src = __ffs(todo) - 1;
+    const int64_t sum = paged_units_warp<M, TK>(a, __shfl_sync(0xffffffffu, b, src));
+    if ((int)(threadIdx.x & 31) == src) u = sum;
+  }
+  return u * a.Hkv;
+}
 
-// CTA `cta` of `ctas` that have work (no more of them than units).
+// CTA c of `ctas` that have work (no more of them than units).
 struct PagedShare {
   int64_t total;
   int ctas;
@@ -178,10 +218,19 @@ struct PagedShare {
   __device__ __forceinline__ int owner(int64_t u) const { return (int)(((u + 1) * ctas - 1) / total); }
 };
 
-// Every thread of the CTA calls it; scan: shared, 34 values.  A CTA beyond
-// the last with work gets b = -1.
+// Where a CTA's share begins: found once by the whole CTA.
+struct PagedStart {
+  int b, h, mt, t;  // b = -1: no share
+};
+struct PagedScratch {
+  int64_t scan[33];  // sums of the warps; [32]: of the CTA
+  int64_t first;     // units before the found request
+  PagedStart st;
+};
+
+// Every thread of the CTA calls it.
 template <int M, int TK>
-__device__ __forceinline__ PagedStart paged_start(const PagedLaunch& a, PagedShare* share, int64_t* scan) {
+__device__ __forceinline__ PagedStart paged_start(const PagedLaunch& a, PagedShare* share, PagedScratch* x) {
   const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nthr >> 5;
   auto inclusive = [&](int64_t v) {  // over the CTA's threads; scan[32]: their sum
 #pragma unroll
@@ -190,50 +239,71 @@ __device__ __forceinline__ PagedStart paged_start(const PagedLaunch& a, PagedSha
       if (lane >= o) v += w;
     }
     __syncthreads();
-    if (lane == 31) scan[warp] = v;
+    if (lane == 31) x->scan[warp] = v;
     __syncthreads();
     int64_t before = 0, all = 0;
     for (int w = 0; w < warps; ++w) {
-      if (w < warp) before += scan[w];
-      all += scan[w];
+      const int64_t y = x->scan[w];
+      if (w < warp) before += y;
+      all += y;
     }
+    if (tid == 0) x->scan[32] = all;
     __syncthreads();
-    scan[32] = all;
     return v + before;
   };
-  PagedStart st;
-  int64_t mine = 0;
-  for (int b = tid; b < a.B; b += nthr) mine += paged_units<M, TK>(a, b) * a.Hkv;
-  inclusive(mine);
-  __syncthreads();
-  st.total = scan[32];
-  st.b = -1;
-  st.first = 0;
-  share->total = st.total;
-  share->ctas = (int)min((int64_t)gridDim.x, st.total);
-  if ((int)blockIdx.x >= share->ctas) return st;  // the same for the whole CTA
-  const int64_t u0 = share->begin(blockIdx.x);
-  int64_t base = 0;
-  __shared__ int found;
-  __shared__ int64_t found_first;
-  if (tid == 0) found = -1;
-  __syncthreads();
+  if (tid == 0) x->st.b = -1;
+  int64_t total = 0;
   for (int b0 = 0; b0 < a.B; b0 += nthr) {
-    const int b = b0 + tid;
-    const int64_t u = b < a.B ? paged_units<M, TK>(a, b) * a.Hkv : 0;
-    const int64_t end = base + inclusive(u);
-    if (end - u <= u0 && u0 < end) {  // one thread at most
-      found = b;
-      found_first = end - u;
+    inclusive(paged_units<M, TK>(a, b0 + tid < a.B ? b0 + tid : a.B));
+    total += x->scan[32];
+  }
+  share->total = total;
+  share->ctas = (int)min((int64_t)gridDim.x, total);
+  if ((int)blockIdx.x < share->ctas) {  // the same for the whole CTA
+    const int64_t u0 = share->begin(blockIdx.x);
+    int64_t base = 0;
+    for (int b0 = 0; b0 < a.B; b0 += nthr) {
+      const int b = b0 + tid;
+      const int64_t u = paged_units<M, TK>(a, b < a.B ? b : a.B);
+      const int64_t end = base + inclusive(u);
+      if (end - u <= u0 && u0 < end) {  // one thread at most
+        x->st.b = b;
+        x->first = end - u;
+      }
+      base += x->scan[32];
+      if (base > u0) break;
     }
     __syncthreads();
-    base += scan[32];
-    if (found >= 0) break;
-    __syncthreads();
+    if (warp == 0) {  // the head, row block and tile
+      const int b = x->st.b;
+      const PagedSeq s = paged_seq(a, b);
+      const int prefix = paged_prefix(a, b);
+      const int64_t per_head = paged_units_warp<M, TK>(a, b);
+      int64_t off = (u0 - x->first) % per_head;
+      const int h = (int)((u0 - x->first) / per_head);
+      for (int m0 = 0;; m0 += 32) {
+        const int c = paged_tile_count<M, TK>(a, s, prefix, m0 + lane);
+        int64_t upto = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += y;
+        }
+        const bool here = upto - c <= off && off < upto;
+        if (here) {
+          int t0, t1;
+          paged_tiles<M, TK>(a, s, prefix, m0 + lane, &t0, &t1);
+          x->st.h = h;
+          x->st.mt = m0 + lane;
+          x->st.t = t0 + (int)(off - (upto - c));
+        }
+        if (__any_sync(0xffffffffu, here)) break;
+        off -= __shfl_sync(0xffffffffu, upto, 31);
+      }
+    }
   }
-  st.b = found;
-  st.first = found_first;
-  return st;
+  __syncthreads();
+  return x->st;
 }
 
 // The pieces of a CTA's share, one after another.  Every thread that walks
@@ -254,30 +324,17 @@ struct PagedWalk {
   int64_t p_item0, p_item1;  // units of the call of its item
 
   __device__ __forceinline__ PagedWalk(const PagedLaunch& a_, const PagedStart& st, const PagedShare& sh)
-      : a(a_), share(sh) {
-    left = 0;
-    if (st.b < 0) return;
+      : a(a_), share(sh), left(0), b(st.b), h(st.h), mt(st.mt), t(st.t) {
+    if (b < 0) return;
     unit = share.begin(blockIdx.x);
     left = share.begin(blockIdx.x + 1) - unit;
-    b = st.b;
     s = paged_seq(a, b);
     prefix = paged_prefix(a, b);
-    int64_t off = unit - st.first;
-    const int64_t per_head = paged_units<M, TK>(a, b);
-    h = (int)(off / per_head);
-    off %= per_head;
-    for (mt = 0;; ++mt) {
-      int t0, t1;
-      paged_tiles<M, TK>(a, s, prefix, mt, &t0, &t1);
-      if (off < t1 - t0) {
-        t = t0 + (int)off;
-        break;
-      }
-      off -= t1 - t0;
-    }
   }
 
-  __device__ __forceinline__ bool next() {
+  // Not inlined, so that the walk lies in local memory between pieces and its
+  // state takes no registers from the tile loops.
+  __device__ __noinline__ bool next() {
     if (left <= 0) return false;
     int t0, t1;
     paged_tiles<M, TK>(a, s, prefix, mt, &t0, &t1);
@@ -345,8 +402,8 @@ __device__ __forceinline__ float paged_cap(float x, float cap) {
 template <int D>
 __device__ __forceinline__ void paged_write(const PagedLaunch& a, const PagedSeq& s, int h, int row, int d, float o,
                                             float top, float l) {
-  const int head = h * a.G + row % a.G;
-  const int64_t at = (s.q0 + row / a.G) * a.Hq + head;
+  const int i = paged_div(a, row), head = h * a.G + row - i * a.G;
+  const int64_t at = (s.q0 + i) * a.Hq + head;
   if (a.sink && s.L > 0) {
     const float sg = a.sink[head] * kPagedLog2e, m = fmaxf(top, sg);
     const float f = paged_ex2(top - m);  // top -inf: 0

@@ -56,6 +56,12 @@ __device__ __forceinline__ uint32_t swz(int row, int byte) {
 template <int W>
 constexpr Swizzle kSwOf = W == 128 ? kSw128 : kSw64;
 
+// 16-byte store to shared memory (the pointers of a swizzled buffer lose their
+// address space on the way, and a generic store costs more).
+__device__ __forceinline__ void st_shared16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
 // 2^e, e clamped to the normal range.
 __device__ __forceinline__ float pow2(int e) {
   e = e < -126 ? -126 : (e > 127 ? 127 : e);
@@ -66,6 +72,16 @@ __device__ __forceinline__ float warp_redux_max(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
+}
+
+// True for one thread of a converged warp.  The compiler knows a branch on it as
+// one thread's, and keeps the operands of tcgen05 instructions inside in
+// uniform registers; under `lane == 0` it moves each there, which made an MMA
+// cost about 110 cycles to issue.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 
 // Barrier `id` over n threads; true for all of them if `ok` is true for all.
@@ -79,15 +95,35 @@ __device__ __forceinline__ bool named_and(int id, int n, bool ok) {
   return r != 0;
 }
 
+// mbar_wait that sleeps between polls, 16 of them between two looks at the
+// clock: a polling warp takes issue slots and instruction fetches from the
+// softmax warps of its scheduler.
+__device__ __forceinline__ bool wait_asleep(uint64_t* bar, uint32_t parity, uint32_t ns, int32_t* status,
+                                            uint64_t limit_ns) {
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+      __nanosleep(ns);
+      if (mbar_try_wait(bar, parity)) return true;
+    }
+    if (global_timer_ns() - t0 > limit_ns) {
+      if (status) atomicOr(status, LCSC_DEV_TIMEOUT);
+      return false;
+    }
+  }
+}
+
 // Bounded wait of a whole warp; false for every lane if one gave up or the CTA has.
 struct Waits {
   int32_t* status;
   uint64_t limit_ns;
   volatile int* abort;
+  uint32_t ns;  // of sleep between polls
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
     if (*abort) return false;
-    bool ok = mbar_wait(bar, parity, status, limit_ns);
-    ok = __all_sync(0xffffffffu, ok);
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const bool ok = __all_sync(0xffffffffu, wait_asleep(bar, parity, ns, status, limit_ns));
     if (!ok && (threadIdx.x & 31) == 0) *abort = 1;
     return ok;
   }
@@ -97,10 +133,10 @@ struct Waits {
 // computes it), and the first tile of the piece that holds one.
 template <int M, int TK>
 struct PieceKeys {
-  int lo, hi, t0;
+  int lo, hi, t0, t1;
   __device__ __forceinline__ PieceKeys(const PagedLaunch& a, const PagedWalk<M, TK>& w) {
     const int prefix = paged_prefix(a, w.p_b), r0 = w.p_mt * M, r1 = r0 + w.rows() - 1;
-    const int i0 = r0 / a.G, i1 = r1 / a.G;
+    const int i0 = paged_div(a, r0), i1 = paged_div(a, r1);
     int x;
     paged_span(a, w.p_s, prefix, i0, &lo, &x);
     paged_span(a, w.p_s, prefix, i1, &x, &hi);
@@ -109,7 +145,50 @@ struct PieceKeys {
       for (int i = i0 + (threadIdx.x & 31); i <= i1; i += 32) d = min(d, a.docs[w.p_s.q0 + i]);
       lo = max(lo, __reduce_min_sync(0xffffffffu, d));
     }
-    t0 = min(w.p_t1, max(w.p_t0, lo / TK));
+    t1 = w.p_t1;
+    t0 = min(t1, max(w.p_t0, lo / TK));
+  }
+};
+
+// Loads under a condition whose results nothing looks at before they are used
+// (a select behind the load would wait for it).
+__device__ __forceinline__ int32_t ld_if(const int32_t* p, bool cond, int32_t other) {
+  int32_t v;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.b32 %0, %3;\n\t@p ld.global.b32 %0, [%1];\n\t}"
+               : "=&r"(v)
+               : "l"(p), "r"((uint32_t)cond), "r"(other));
+  return v;
+}
+__device__ __forceinline__ float ld_if(const float* p, bool cond, float other) {
+  return __int_as_float(ld_if(reinterpret_cast<const int32_t*>(p), cond, __float_as_int(other)));
+}
+__device__ __forceinline__ uint4 ld_if(const uint8_t* p, bool cond) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
+      "mov.b32 %3, 0;\n\t@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"((uint32_t)cond));
+  return v;
+}
+
+// Page lookups run ahead of their use: the table's entry is loaded a tile before
+// the page's scale or codes are asked for, and nothing looks at a loaded value
+// before the next tile, so that no load is waited for.
+template <int M, int TK>
+struct PageAhead {
+  const PagedLaunch& a;
+  const int32_t* table;
+  int lo, hi, end, h;  // keys looked at, and the tile the piece ends before
+  __device__ __forceinline__ PageAhead(const PagedLaunch& a_, const PagedWalk<M, TK>& w, const PieceKeys<M, TK>& k)
+      : a(a_), table(a_.table + (int64_t)w.p_b * a_.max_blocks), lo(k.lo), hi(k.hi), end(k.t1), h(w.p_h) {}
+  // Table entry of key j of tile t (-1: no page of this piece).
+  __device__ __forceinline__ int32_t entry(int t, int j) const {
+    return ld_if(table + (j >> a.page_log2), t < end && j < hi && (j | (a.page - 1)) >= lo, -1);
+  }
+  // Its (page, head), or -1.
+  __device__ __forceinline__ int64_t place(int32_t e) const {
+    return e >= 0 && e < a.n_pages ? (int64_t)e * a.Hkv + h : -1;
   }
 };
 
@@ -162,8 +241,8 @@ struct FewCfg {
   static constexpr int OFF_RED = OFF_QS + NR * 4;     // float [4][NR]
   static constexpr int OFF_VMAX = OFF_RED + 4 * NR * 4;  // int [4]
   static constexpr int OFF_M = OFF_VMAX + 16;         // float [NR]
-  static constexpr int OFF_SCAN = OFF_M + NR * 4;     // int64 [34]
-  static constexpr int OFF_TM = OFF_SCAN + 34 * 8;
+  static constexpr int OFF_SCAN = OFF_M + NR * 4;     // PagedScratch
+  static constexpr int OFF_TM = OFF_SCAN + (int)sizeof(PagedScratch);
   static constexpr int OFF_ABORT = OFF_TM + 4;
   static constexpr int SMEM = OFF_ABORT + 4 + 1024;
   static_assert(kBars % 2 == 0 && OFF_F4 % 16 == 0 && OFF_F2 % 8 == 0 && OFF_ROW % 16 == 0 && OFF_SCAN % 8 == 0, "alignment");
@@ -174,7 +253,7 @@ struct FewCfg {
 
 template <int D, int NR>
 __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
-    paged_few_kernel(const PagedLaunch a, const __grid_constant__ CUtensorMap map_k,
+    paged_few_kernel(const __grid_constant__ PagedLaunch a, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const WaitTest test) {
   using C = FewCfg<D, NR>;
   constexpr int TK = C::TK, N = C::N, PW = C::PW, NS = C::kStages;
@@ -198,7 +277,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
   uint32_t* tm_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_TM);
   volatile int* abort = reinterpret_cast<volatile int*>(sm + C::OFF_ABORT);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const Waits wait{a.status, test.limit_ns, abort};
+  const Waits wait{a.status, test.limit_ns, abort, 40u};
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
@@ -212,7 +291,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
   }
   if (warp == 5) tmem_alloc(tm_slot, C::kCols);
   PagedShare share;
-  const PagedStart st = paged_start<NR, TK>(a, &share, reinterpret_cast<int64_t*>(sm + C::OFF_SCAN));
+  const PagedStart st = paged_start<NR, TK>(a, &share, reinterpret_cast<PagedScratch*>(sm + C::OFF_SCAN));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -228,30 +307,26 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
     bool go = true;
     while (go && w.next()) {
       const PieceKeys<NR, TK> keys(a, w);
-      const int32_t* table = a.table + (int64_t)w.p_b * a.max_blocks;
-      // lane i < per: the tile's page i, loaded a tile ahead; -1: not copied
-      auto page_of = [&](int t) -> int32_t {
-        const int j = t * TK + lane * a.page;
-        if (lane >= per || t >= w.p_t1 || j >= keys.hi || j + a.page <= keys.lo) return -1;
-        const int32_t pg = table[j >> a.page_log2];
-        if (pg >= 0 && pg < a.n_pages) return pg;
-        if (a.status) atomicOr(a.status, LCSC_DEV_BAD_INDEX);
-        return -1;
-      };
-      int32_t next = page_of(keys.t0);
-      for (int t = keys.t0; t < w.p_t1; ++t, ++n) {
-        const int32_t pg = next;
-        next = page_of(t + 1);
+      const PageAhead<NR, TK> pages(a, w, keys);
+      // lane i < per: the tile's page i
+      auto entry = [&](int t) { return pages.entry(lane < per ? t : INT_MAX, t * TK + lane * a.page); };
+      int32_t e1 = entry(keys.t0), e2 = entry(keys.t0 + 1);
+      for (int t = keys.t0; t < keys.t1; ++t, ++n) {
+        const int64_t ph = pages.place(e1);
+        if (ph < 0 && lane < per && t * TK + lane * a.page < keys.hi && t * TK + (lane + 1) * a.page > keys.lo && a.status)
+          atomicOr(a.status, LCSC_DEV_BAD_INDEX);
+        e1 = e2;
+        e2 = entry(t + 2);
         const int s = n % NS;
         if (n >= NS && !wait(&empty[s], (uint32_t)(n / NS - 1) & 1u)) {
           go = false;
           break;
         }
-        const uint32_t some = __ballot_sync(0xffffffffu, pg >= 0);
+        const uint32_t some = __ballot_sync(0xffffffffu, ph >= 0);
         if (lane == 0) mbar_arrive_expect_tx(&full[s], 2 * page_bytes * __popc(some));
         __syncwarp();
-        if (pg >= 0) {
-          const int32_t row = (int32_t)(((int64_t)pg * a.Hkv + w.p_h) << a.page_log2);
+        if (ph >= 0) {
+          const int32_t row = (int32_t)(ph << a.page_log2);
           tma_load_2d(sm + C::OFF_K + s * C::kTile + lane * page_bytes, &map_k, 0, row, &full[s]);
           tma_load_2d(sm + C::OFF_V + s * C::kTile + lane * page_bytes, &map_v, 0, row, &full[s]);
         }
@@ -274,7 +349,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
     auto issue_pv = [&](int m) -> bool {
       if (!wait(p_full, (uint32_t)m & 1u)) return false;
       tc_fence_after();
-      if (lane == 0) {
+      if (elect_one()) {
         const uint32_t va = smem_u32(sm + C::OFF_V + (m % NS) * C::kTile);
 #pragma unroll
         for (int k = 0; k < TK / 32; ++k)
@@ -296,11 +371,11 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
       pend = false;
       if (!(go = wait(q_full, (uint32_t)pieces & 1u))) break;
       ++pieces;
-      for (int t = keys.t0; t < w.p_t1; ++t) {
+      for (int t = keys.t0; t < keys.t1; ++t) {
         const int s = n % NS;
         if (!(go = wait(&full[s], (uint32_t)(n / NS) & 1u))) break;
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
           const uint32_t ka = smem_u32(sm + C::OFF_K + s * C::kTile);
 #pragma unroll
           for (int term = 0; term < kQTerms; ++term)
@@ -339,11 +414,11 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
       if (tid < NR) {
         int4 r = make_int4(0, 0, 0, 0);
         if (tid < rows) {
-          const int i = (r0 + tid) / a.G;
+          const int i = paged_div(a, r0 + tid);
           paged_span(a, w.p_s, paged_prefix(a, w.p_b), i, &r.x, &r.y);
           r.z = w.p_s.L - w.p_s.n + i;
           if (a.docs) r.x = max(r.x, a.docs[w.p_s.q0 + i]);
-          if (a.slopes) r.w = __float_as_int(a.slopes[w.p_h * a.G + (r0 + tid) % a.G] * kPagedLog2e);
+          if (a.slopes) r.w = __float_as_int(a.slopes[w.p_h * a.G + r0 + tid - i * a.G] * kPagedLog2e);
         }
         row_s[tid] = r;
       }
@@ -355,9 +430,9 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
 #pragma unroll
           for (int i = 0; i < VPL; ++i) v[i] = 0.f;
           if (r < rows) {
-            const int row = r0 + r;
-            const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q) + (w.p_s.q0 + row / a.G) * a.q_stride +
-                                (int64_t)(w.p_h * a.G + row % a.G) * D + lane * VPL;
+            const int row = r0 + r, tok = paged_div(a, row);
+            const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q) + (w.p_s.q0 + tok) * a.q_stride +
+                                (int64_t)(w.p_h * a.G + row - tok * a.G) * D + lane * VPL;
             if constexpr (VPL == 4) {
               const uint2 u = *reinterpret_cast<const uint2*>(p);
               v[0] = bf16_val((uint16_t)u.x), v[1] = bf16_val((uint16_t)(u.x >> 16));
@@ -405,16 +480,11 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
 #pragma unroll
       for (int r = 0; r < NR; ++r) l[r] = 0.f, o[r] = 0.f;
       float m_run = -INFINITY;  // thread r < NR: running max of row r
-      const int32_t* table = a.table + (int64_t)w.p_b * a.max_blocks;
       // this thread's key of a tile: its page two tiles ahead, its scales one
-      auto page_of = [&](int t) -> int64_t {
-        const int j = t * TK + tid;
-        if (t >= w.p_t1 || j >= keys.hi || (j | (a.page - 1)) < keys.lo) return -1;
-        const int32_t pg = table[j >> a.page_log2];
-        return pg >= 0 && pg < a.n_pages ? (int64_t)pg * a.Hkv + w.p_h : -1;
-      };
-      int64_t ph = page_of(keys.t0), ph_next = page_of(keys.t0 + 1);
-      float ks = ph < 0 ? -1.f : a.k_scale[ph], vs = ph < 0 ? 0.f : a.v_scale[ph];
+      const PageAhead<NR, TK> pages(a, w, keys);
+      const int64_t ph0 = pages.place(pages.entry(keys.t0, keys.t0 * TK + tid));
+      int32_t e1 = pages.entry(keys.t0 + 1, (keys.t0 + 1) * TK + tid);
+      float ks = ph0 < 0 ? -1.f : a.k_scale[ph0], vs = ph0 < 0 ? 0.f : a.v_scale[ph0];
       auto add_o = [&](int m) -> bool {  // O of tile m into the running one
         if (!wait(o_full, (uint32_t)m & 1u)) return false;
         tc_fence_after();
@@ -428,9 +498,10 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
         }
         return true;
       };
-      for (int t = keys.t0; t < w.p_t1; ++t, ++n) {
-        const float ks_next = ph_next < 0 ? -1.f : a.k_scale[ph_next], vs_next = ph_next < 0 ? 0.f : a.v_scale[ph_next];
-        ph_next = page_of(t + 2);
+      for (int t = keys.t0; t < keys.t1; ++t, ++n) {
+        const int64_t ph1 = pages.place(e1);
+        const float ks_next = ld_if(a.k_scale + ph1, ph1 >= 0, -1.f), vs_next = ld_if(a.v_scale + ph1, ph1 >= 0, 0.f);
+        e1 = pages.entry(t + 2, (t + 2) * TK + tid);
         const int j = t * TK + tid;
         const bool there = ks >= 0.f && j < keys.hi;  // copied, and of this request
         const bool seen = there && j >= keys.lo;
@@ -476,7 +547,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
         if (tid < NR) f2_s[tid] = make_float2(al, be * vmax * (1.f / 256.f));
         // weights in [0, 256], relative to the tile's maxima and largest V scale
         const float vr = there && vmax > 0.f ? __fdividef(vs, vmax) * 256.f : 0.f;
-        uint8_t* prow = sm + C::OFF_P;
+        const uint32_t prow = smem_u32(sm + C::OFF_P);
 #pragma unroll
         for (int r8 = 0; r8 < N; r8 += 16) {
           uint32_t code[kPTerms][4];
@@ -504,8 +575,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
           }
 #pragma unroll
           for (int term = 0; term < kPTerms; ++term)
-            *reinterpret_cast<uint4*>(prow + swz<PW>(tid, term * N + r8)) =
-                make_uint4(code[term][0], code[term][1], code[term][2], code[term][3]);
+            st_shared16(prow + swz<PW>(tid, term * N + r8), code[term][0], code[term][1], code[term][2], code[term][3]);
         }
         if (!there) {  // no such key: its V row may hold anything, and 0 x NaN is NaN
           uint4* v = reinterpret_cast<uint4*>(sm + C::OFF_V + (n % NS) * C::kTile + tid * D);
@@ -594,8 +664,8 @@ struct ManyCfg {
   static constexpr int OFF_P = OFF_V + 2 * kV;        // [2 tiles]
   static constexpr int OFF_BAR = OFF_P + 2 * kP;
   static constexpr int kBars = 18;
-  static constexpr int OFF_SCAN = OFF_BAR + kBars * 8;  // int64 [34]
-  static constexpr int OFF_VREF = OFF_SCAN + 34 * 8;    // int: largest V scale of the piece (bits)
+  static constexpr int OFF_SCAN = OFF_BAR + kBars * 8;  // PagedScratch
+  static constexpr int OFF_VREF = OFF_SCAN + (int)sizeof(PagedScratch);    // int: largest V scale of the piece (bits)
   static constexpr int OFF_TM = OFF_VREF + 4;
   static constexpr int OFF_ABORT = OFF_TM + 4;
   static constexpr int SMEM = OFF_ABORT + 4 + 1024;
@@ -609,23 +679,53 @@ struct ManyRow {
   float rf, slope;  // sm_scale log2(e) 2^e of the query; bias per position in base-2 units
 };
 
-// 16 raw products of the keys j .. j + 15 (page scale ks; < 0: not there) to scores in base-2 units.
-__device__ __forceinline__ void many_scores(const PagedLaunch& a, const ManyRow& r, float cap2, float ks, int j,
-                                            bool inside, const uint32_t* x, float* y) {
-  const float c = ks * r.rf;
+// Bits of the keys j .. j + 31 that the row sees; `there`: bit i for a page of the keys j + 16 i ..
+__device__ __forceinline__ uint32_t many_seen(const ManyRow& r, int j, uint32_t there) {
+  const int lo = min(max(r.lo - j, 0), 32), hi = min(max(r.hi - j, 0), 32);
+  const uint32_t below_hi = (uint32_t)((1ull << hi) - 1), below_lo = (uint32_t)((1ull << lo) - 1);
+  return below_hi & ~below_lo & ((there & 1u ? 0x0000ffffu : 0u) | (there & 2u ? 0xffff0000u : 0u));
+}
+
+// A tile's scores in base-2 units for a thread's row, 32 keys a step, handed
+// to `use` with their first key's number in the tile and the factors that the
+// first and the last 16 still lack.  Three forms, each a
+// rolled loop: the whole loop body of a softmax warp has to stay in the
+// instruction cache (rolled against unrolled fourfold, chunk of 4096 tokens:
+// 1,220 against 1,470 us).
+//   kPlain:  every row of the warp sees every key, no cap, no bias
+//   kMasked: no cap, no bias
+//   kScores: everything
+enum ManyForm { kPlain, kMasked, kScores };
+template <ManyForm F, class Use>
+__device__ __forceinline__ void many_scores(const PagedLaunch& a, const ManyRow& r, float cap2, float ks, int j0,
+                                            uint32_t s_addr, Use use) {
+#pragma unroll 1
+  for (int h = 0; h < 128; h += 32) {
+    uint32_t x[32];
+    tmem_ld(s_addr + h, x);
+    const float k0 = __shfl_sync(0xffffffffu, ks, h >> 4), k1 = __shfl_sync(0xffffffffu, ks, (h >> 4) + 1);
+    uint32_t seen = 0xffffffffu;
+    if constexpr (F != kPlain) seen = many_seen(r, j0 + h, (k0 >= 0.f ? 1u : 0u) | (k1 >= 0.f ? 2u : 0u));
+    const float c0 = k0 * r.rf, c1 = k1 * r.rf;
+    tmem_ld_done(x);
+    if constexpr (F != kPlain) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    float v = __uint_as_float(x[i]) * c;
-    if (a.cap > 0.f) v = paged_cap(v, cap2);
-    if (a.slopes) v -= r.slope * (float)abs(r.pos - (j + i));
-    if (!inside && !(ks >= 0.f && j + i >= r.lo && j + i < r.hi)) v = -INFINITY;
-    y[i] = v;
+      for (int i = 0; i < 32; ++i) {
+        float v = __uint_as_float(x[i]) * (i < 16 ? c0 : c1);
+        if constexpr (F == kScores) {
+          if (a.cap > 0.f) v = paged_cap(v, cap2);
+          if (a.slopes) v -= r.slope * (float)abs(r.pos - (j0 + h + i));
+        }
+        x[i] = __float_as_uint(seen >> i & 1u ? v : -INFINITY);
+      }
+    }
+    use(h, x, F == kPlain ? c0 : 1.f, F == kPlain ? c1 : 1.f);
   }
 }
 
 template <int D>
 __global__ void __launch_bounds__(kManyThreads, 1)
-    paged_many_kernel(const PagedLaunch a, const __grid_constant__ CUtensorMap map_k, const WaitTest test) {
+    paged_many_kernel(const __grid_constant__ PagedLaunch a, const __grid_constant__ CUtensorMap map_k, const WaitTest test) {
   using C = ManyCfg<D>;
   constexpr int TK = C::TK, M = kManyRows;
   grid_dep_wait();
@@ -646,7 +746,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   uint32_t* tm_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_TM);
   volatile int* abort = reinterpret_cast<volatile int*>(sm + C::OFF_ABORT);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const Waits wait{a.status, test.limit_ns, abort};
+  const Waits wait{a.status, test.limit_ns, abort, warp == 13 ? 20u : warp >= 8 ? 100u : 50u};
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -663,7 +763,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   }
   if (warp == 13) tmem_alloc(tm_slot, 512);
   PagedShare share;
-  const PagedStart st = paged_start<M, TK>(a, &share, reinterpret_cast<int64_t*>(sm + C::OFF_SCAN));
+  const PagedStart st = paged_start<M, TK>(a, &share, reinterpret_cast<PagedScratch*>(sm + C::OFF_SCAN));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -678,30 +778,26 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     bool go = true;
     while (go && w.next()) {
       const PieceKeys<M, TK> keys(a, w);
-      const int32_t* table = a.table + (int64_t)w.p_b * a.max_blocks;
-      auto page_of = [&](int t) -> int32_t {
-        const int j = t * TK + lane * a.page;
-        if (lane >= per || t >= w.p_t1 || j >= keys.hi || j + a.page <= keys.lo) return -1;
-        const int32_t pg = table[j >> a.page_log2];
-        if (pg >= 0 && pg < a.n_pages) return pg;
-        if (a.status) atomicOr(a.status, LCSC_DEV_BAD_INDEX);
-        return -1;
-      };
-      int32_t next = page_of(keys.t0);
-      for (int t = keys.t0; t < w.p_t1; ++t, ++n) {
-        const int32_t pg = next;
-        next = page_of(t + 1);
+      const PageAhead<M, TK> pages(a, w, keys);
+      // lane i < per: the tile's page i
+      auto entry = [&](int t) { return pages.entry(lane < per ? t : INT_MAX, t * TK + lane * a.page); };
+      int32_t e1 = entry(keys.t0), e2 = entry(keys.t0 + 1);
+      for (int t = keys.t0; t < keys.t1; ++t, ++n) {
+        const int64_t ph = pages.place(e1);
+        if (ph < 0 && lane < per && t * TK + lane * a.page < keys.hi && t * TK + (lane + 1) * a.page > keys.lo && a.status)
+          atomicOr(a.status, LCSC_DEV_BAD_INDEX);
+        e1 = e2;
+        e2 = entry(t + 2);
         const int s = n & 1;
         if (n >= 2 && !wait(&k_empty[s], (uint32_t)((n >> 1) - 1) & 1u)) {
           go = false;
           break;
         }
-        const uint32_t some = __ballot_sync(0xffffffffu, pg >= 0);
+        const uint32_t some = __ballot_sync(0xffffffffu, ph >= 0);
         if (lane == 0) mbar_arrive_expect_tx(&k_full[s], page_bytes * __popc(some));
         __syncwarp();
-        if (pg >= 0)
-          tma_load_2d(sm + C::OFF_K + s * C::kK + lane * page_bytes, &map_k, 0,
-                      (int32_t)(((int64_t)pg * a.Hkv + w.p_h) << a.page_log2), &k_full[s]);
+        if (ph >= 0)
+          tma_load_2d(sm + C::OFF_K + s * C::kK + lane * page_bytes, &map_k, 0, (int32_t)(ph << a.page_log2), &k_full[s]);
         __syncwarp();
       }
     }
@@ -716,7 +812,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     bool go = !test.stall || wait(drain, 0);  // a test of the failure path: nothing has committed to it yet
     int n = 0, pieces = 0, cnt[2] = {0, 0};
     auto issue_pv = [&](int g, bool last, bool acc) {  // P V of tile n - 1 (its P and V are there)
-      if (lane == 0) {
+      if (elect_one()) {
         const int b = (n - 1) & 1;
         const uint32_t pa = smem_u32(sm + C::OFF_P + g * C::kP), va = smem_u32(sm + C::OFF_V + b * C::kV);
 #pragma unroll
@@ -734,13 +830,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const int tiles = w.rows() > 128 ? 2 : 1;
       if (!(go = wait(q_full, (uint32_t)pieces & 1u))) break;
       ++pieces;
-      for (int t = keys.t0; go && t < w.p_t1; ++t) {
+      for (int t = keys.t0; go && t < keys.t1; ++t) {
         const int s = n & 1;
         if (!(go = wait(&k_full[s], (uint32_t)(n >> 1) & 1u))) break;
         for (int g = 0; g < tiles; ++g) {
           if (t > keys.t0 && !(go = wait(&p_full[g], (uint32_t)(cnt[g] - 1) & 1u))) break;
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             const uint32_t ka = smem_u32(sm + C::OFF_K + s * C::kK);
 #pragma unroll
             for (int term = 0; term < kQTerms; ++term)
@@ -783,7 +879,6 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     bool ok = true;
     while (ok && w.next()) {
       const PieceKeys<M, TK> keys(a, w);
-      const int32_t* table = a.table + (int64_t)w.p_b * a.max_blocks;
       if (keys.t0 >= w.p_t1) {
         // nothing to do, but the piece counts
         ok = named_and(2, 128, true);
@@ -792,17 +887,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         if (ok && lane == 0) mbar_arrive(ref_full);
         continue;
       }
-      // (page, head) of a key, or -1
-      auto page_of = [&](int j) -> int64_t {
-        if (j >= keys.hi || (j | (a.page - 1)) < keys.lo) return -1;
-        const int32_t pg = table[j >> a.page_log2];
-        return pg >= 0 && pg < a.n_pages ? (int64_t)pg * a.Hkv + w.p_h : -1;
-      };
+      const PageAhead<M, TK> pages(a, w, keys);
       // the largest scale of the piece's pages
       int top = 0;
       for (int j = max(keys.t0 * TK, keys.lo / a.page * a.page) + (tid - 256) * a.page; j < min(keys.hi, w.p_t1 * TK);
            j += 128 * a.page) {
-        const int64_t ph = page_of(j);
+        const int64_t ph = pages.place(pages.entry(keys.t0, j));
         if (ph >= 0) top = max(top, __float_as_int(a.v_scale[ph]));
       }
       top = __reduce_max_sync(0xffffffffu, top);
@@ -818,26 +908,30 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const float inv = vref > 0.f ? __fdividef(1.f, vref) * 32768.f : 0.f;
       uint4 raw[IT];
       float sc[2];  // scales of the warp's keys 0-15 and 16-31 (0: not there)
+      int32_t e[2];  // pages of the same keys of the tile to fetch next
+      auto entries = [&](int t) {
+        e[0] = pages.entry(t, t * TK + v * 32);
+        e[1] = pages.entry(t, t * TK + v * 32 + 16);
+      };
       auto fetch = [&](int t) {
-        if (t >= w.p_t1) return;
         const int j0 = t * TK + v * 32;
-        const int64_t p0 = page_of(j0), p1 = page_of(j0 + 16);
-        sc[0] = p0 < 0 ? 0.f : a.v_scale[p0];
-        sc[1] = p1 < 0 ? 0.f : a.v_scale[p1];
+        const int64_t p0 = pages.place(e[0]), p1 = pages.place(e[1]);
+        sc[0] = ld_if(a.v_scale + p0, p0 >= 0, 0.f);
+        sc[1] = ld_if(a.v_scale + p1, p1 >= 0, 0.f);
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
           const int r = i * RPI + rsub, j = j0 + r;
           const int64_t ph = i < IT / 2 ? p0 : p1;
-          raw[i] = make_uint4(0, 0, 0, 0);
-          if (ph >= 0 && j < keys.hi)
-            raw[i] = *reinterpret_cast<const uint4*>(a.v + (ph * a.page + (j & (a.page - 1))) * D + c * 16);
+          raw[i] = ld_if(a.v + (ph * a.page + (j & (a.page - 1))) * D + c * 16, ph >= 0 && j < keys.hi);
         }
       };
+      entries(keys.t0);
       fetch(keys.t0);
-      for (int t = keys.t0; t < w.p_t1; ++t, ++n) {
+      entries(keys.t0 + 1);
+      for (int t = keys.t0; t < keys.t1; ++t, ++n) {
         const int b = n & 1;
         if (n >= 2 && !(ok = wait(&v_empty[b], (uint32_t)((n >> 1) - 1) & 1u))) break;
-        uint8_t* dst = sm + C::OFF_V + b * C::kV;
+        const uint32_t dst = smem_u32(sm + C::OFF_V + b * C::kV);
         // codes to f16 (exact), times 2^15 scale / vref / 2^8: the code's bits
         // as an f16 read 2^-8 of its value, so the factor is 2^15 at most
         const __half2 f[2] = {__float2half2_rn(sc[0] * inv), __float2half2_rn(sc[1] * inv)};
@@ -860,15 +954,16 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           // atom store theirs in the other order, so that a store covers all banks
           const int r = v * 32 + i * RPI + rsub, atom = c / 4, ch = (c % 4) * 2;
           const bool flip = (c / 4) & 1;
-          uint8_t* at = dst + atom * (TK * 128);
+          const uint32_t at = dst + atom * (TK * 128);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const bool second = (q == 1) != flip;
-            *reinterpret_cast<uint4*>(at + swz<128>(r, (ch + (second ? 1 : 0)) * 16)) =
-                second ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(h[0], h[1], h[2], h[3]);
+            st_shared16(at + swz<128>(r, (ch + (second ? 1 : 0)) * 16), second ? h[4] : h[0], second ? h[5] : h[1],
+                        second ? h[6] : h[2], second ? h[7] : h[3]);
           }
         }
         fetch(t + 1);
+        entries(t + 2);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&v_full[b]);
@@ -892,11 +987,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const bool mine = g * 128 + row_in < rows, tile_live = g * 128 < rows;
       ManyRow r = {0, INT_MAX, 0, 0.f, 0.f};
       if (mine) {
-        const int i = (r0 + row_in) / a.G;
+        const int i = paged_div(a, r0 + row_in);
         paged_span(a, w.p_s, paged_prefix(a, w.p_b), i, &r.lo, &r.hi);
         r.pos = w.p_s.L - w.p_s.n + i;
         if (a.docs) r.lo = max(r.lo, a.docs[w.p_s.q0 + i]);
-        if (a.slopes) r.slope = a.slopes[w.p_h * a.G + (r0 + row_in) % a.G] * kPagedLog2e;
+        if (a.slopes) r.slope = a.slopes[w.p_h * a.G + r0 + row_in - i * a.G] * kPagedLog2e;
       }
       const bool work = keys.t0 < w.p_t1;
       if (work) {
@@ -913,8 +1008,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 #pragma unroll
               for (int i = 0; i < VPL / 2; ++i) u[q][i] = 0;
               if (g * 128 + ri < rows) {
-                const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q) + (w.p_s.q0 + row / a.G) * a.q_stride +
-                                    (int64_t)(w.p_h * a.G + row % a.G) * D + lane * VPL;
+                const int tok = paged_div(a, row);
+                const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q) + (w.p_s.q0 + tok) * a.q_stride +
+                                    (int64_t)(w.p_h * a.G + row - tok * a.G) * D + lane * VPL;
                 if constexpr (VPL == 4) {
                   const uint2 x = *reinterpret_cast<const uint2*>(p);
                   u[q][0] = x.x, u[q][1] = x.y;
@@ -967,53 +1063,38 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       ++pieces;
       const float vref = __int_as_float(*vref_s);
       float m_ref = -INFINITY, l = 0.f;
-      const int32_t* table = a.table + (int64_t)w.p_b * a.max_blocks;
       // lane i < 8: the page of the tile's keys 16 i .. 16 i + 15, two tiles
       // ahead, and its K scale one ahead
-      auto page_of = [&](int t) -> int64_t {
-        const int j = t * TK + lane * 16;
-        if (lane >= 8 || t >= w.p_t1 || j >= keys.hi || (j | (a.page - 1)) < keys.lo) return -1;
-        const int32_t pg = table[j >> a.page_log2];
-        return pg >= 0 && pg < a.n_pages ? (int64_t)pg * a.Hkv + w.p_h : -1;
-      };
+      const PageAhead<M, TK> pages(a, w, keys);
+      auto entry = [&](int t) { return pages.entry(lane < 8 ? t : INT_MAX, t * TK + lane * 16); };
       if (work && tile_live) {
-        int64_t ph = page_of(keys.t0), ph_next = page_of(keys.t0 + 1);
-        float ks = ph < 0 ? -1.f : a.k_scale[ph];
-        uint8_t* prow = sm + C::OFF_P + g * C::kP;
-        for (int t = keys.t0; t < w.p_t1; ++t) {
-          const float ks_next = ph_next < 0 ? -1.f : a.k_scale[ph_next];
-          ph_next = page_of(t + 2);
+        const int64_t ph0 = pages.place(entry(keys.t0));
+        int32_t e1 = entry(keys.t0 + 1);
+        float ks = ph0 < 0 ? -1.f : a.k_scale[ph0];
+        const uint32_t prow = smem_u32(sm + C::OFF_P + g * C::kP);
+        for (int t = keys.t0; t < keys.t1; ++t) {
+          const int64_t ph1 = pages.place(e1);
+          const float ks_next = ld_if(a.k_scale + ph1, ph1 >= 0, -1.f);
+          e1 = entry(t + 2);
           const int j0 = t * TK;
           const bool inside = __all_sync(0xffffffffu, r.lo <= j0 && r.hi >= j0 + TK && (lane >= 8 || ks >= 0.f));
           if (!(ok = wait(&s_full[g], (uint32_t)cnt & 1u))) break;
           tc_fence_after();
           // the row's maximum over the tile
           float top = -INFINITY;
-          uint32_t x[2][32];
-          tmem_ld(s_addr, x[0]);
+          auto maximum = [&](int, const uint32_t (&x)[32], float c0, float c1) {
+            float m0 = __uint_as_float(x[0]), m1 = __uint_as_float(x[16]);
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            tmem_ld_done(x[h & 1]);
-            if (h < 3) tmem_ld(s_addr + (h + 1) * 32, x[(h + 1) & 1]);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float kg = __shfl_sync(0xffffffffu, ks, 2 * h + e);
-              if (inside && !a.slopes) {
-                float mx = __uint_as_float(x[h & 1][16 * e]);
-#pragma unroll
-                for (int i = 1; i < 16; ++i) mx = fmaxf(mx, __uint_as_float(x[h & 1][16 * e + i]));
-                mx *= kg * r.rf;
-                if (a.cap > 0.f) mx = paged_cap(mx, cap2);
-                top = fmaxf(top, mx);
-              } else {
-                float y[16];
-                many_scores(a, r, cap2, kg, j0 + 32 * h + 16 * e, inside, &x[h & 1][16 * e], y);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, y[i]);
-              }
+            for (int i = 1; i < 16; ++i) {
+              m0 = fmaxf(m0, __uint_as_float(x[i]));
+              m1 = fmaxf(m1, __uint_as_float(x[16 + i]));
             }
-          }
-          tmem_ld(s_addr, x[0]);
+            top = fmaxf(top, fmaxf(m0 * c0, m1 * c1));
+          };
+          const ManyForm form = a.cap > 0.f || a.slopes ? kScores : inside ? kPlain : kMasked;
+          if (form == kPlain) many_scores<kPlain>(a, r, cap2, ks, j0, s_addr, maximum);
+          else if (form == kMasked) many_scores<kMasked>(a, r, cap2, ks, j0, s_addr, maximum);
+          else many_scores<kScores>(a, r, cap2, ks, j0, s_addr, maximum);
           const bool fresh = t == keys.t0;
           float alpha = 1.f;
           bool grown = false;
@@ -1024,13 +1105,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             l *= alpha;
           }
           // P and O: the last tile's P V has read and added to them
-          if (!fresh && !(ok = wait(&pv_done[g], (uint32_t)(cnt - 1) & 1u))) {
-            tmem_ld_done(x[0]);
-            break;
-          }
+          if (!fresh && !(ok = wait(&pv_done[g], (uint32_t)(cnt - 1) & 1u))) break;
           if (__any_sync(0xffffffffu, grown)) {
             tc_fence_after();
-            tmem_ld_done(x[0]);
 #pragma unroll 1
             for (int d = 0; d < D; d += 32) {
               uint32_t o[32];
@@ -1043,40 +1120,29 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             tmem_st_wait();
           }
           const float ref = m_ref == -INFINITY ? 0.f : m_ref;
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            tmem_ld_done(x[h & 1]);
-            if (h < 3) tmem_ld(s_addr + (h + 1) * 32, x[(h + 1) & 1]);
+          auto weights = [&](int h, const uint32_t (&x)[32], float c0, float c1) {
             uint32_t pk[16];
+            float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float kg = __shfl_sync(0xffffffffu, ks, 2 * h + e);
-              float p[16];
-              if (inside && !a.slopes && !(a.cap > 0.f)) {
-                const float c = kg * r.rf;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) p[i] = paged_ex2(fmaf(__uint_as_float(x[h & 1][16 * e + i]), c, -ref));
-              } else {
-                many_scores(a, r, cap2, kg, j0 + 32 * h + 16 * e, inside, &x[h & 1][16 * e], p);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) p[i] = paged_ex2(p[i] - ref);
-              }
-              float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                s0 += p[i];
-                s1 += p[i + 1];
-                const __half2 hp = __floats2half2_rn(p[i], p[i + 1]);
-                pk[8 * e + i / 2] = *reinterpret_cast<const uint32_t*>(&hp);
-              }
-              l += s0 + s1;
+            for (int i = 0; i < 32; i += 2) {
+              const float c = i < 16 ? c0 : c1;
+              const float p0 = paged_ex2(fmaf(__uint_as_float(x[i]), c, -ref));
+              const float p1 = paged_ex2(fmaf(__uint_as_float(x[i + 1]), c, -ref));
+              s0 += p0;
+              s1 += p1;
+              const __half2 hp = __floats2half2_rn(p0, p1);
+              pk[i / 2] = *reinterpret_cast<const uint32_t*>(&hp);
             }
-            uint8_t* at = prow + (h / 2) * (128 * 128);
+            l += s0 + s1;
+            const uint32_t at = prow + (h >> 6) * (128 * 128);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<uint4*>(at + swz<128>(row_in, (h & 1) * 64 + i * 16)) =
-                  make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-          }
+              st_shared16(at + swz<128>(row_in, (h & 32) * 2 + i * 16), pk[4 * i], pk[4 * i + 1], pk[4 * i + 2],
+                          pk[4 * i + 3]);
+          };
+          if (form == kPlain) many_scores<kPlain>(a, r, cap2, ks, j0, s_addr, weights);
+          else if (form == kMasked) many_scores<kMasked>(a, r, cap2, ks, j0, s_addr, weights);
+          else many_scores<kScores>(a, r, cap2, ks, j0, s_addr, weights);
           fence_async_smem();
           tc_fence_before();
           __syncwarp();
@@ -1092,8 +1158,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       if (tile_live) {
         const float unit = vref * (1.f / 128.f);
         const int row = r0 + row_in;
-        const int head = w.p_h * a.G + row % a.G;
-        const int64_t at = (w.p_s.q0 + row / a.G) * a.Hq + head;
+        const int tok = paged_div(a, row), head = w.p_h * a.G + row - tok * a.G;
+        const int64_t at = (w.p_s.q0 + tok) * a.Hq + head;
         const int64_t part = w.slot() * M + g * 128 + row_in;
         float f = unit;
         if (w.whole()) {
