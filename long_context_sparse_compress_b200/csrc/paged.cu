@@ -600,8 +600,8 @@ __global__ void __launch_bounds__(kFmaThreads) paged_fma_kernel(const __grid_con
 // ---------------------------------------------------------- split items
 // Joins the pieces of an item in CTA order: O = sum_i 2^(m_i - m) O_i and the
 // same for the sums.  The CTA of the item's second piece does it; D threads, a
-// dim each, 8 CTAs per item sharing its rows.
-constexpr int kCombineY = 8;
+// dim each, up to 32 CTAs per item sharing its rows.
+constexpr int kCombineY = 32;
 
 template <int D>
 __global__ void __launch_bounds__(D) paged_combine_kernel(PagedLaunch a, int M) {

@@ -62,6 +62,26 @@ __device__ __forceinline__ void st_shared16(uint32_t at, uint32_t x, uint32_t y,
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
+// Two float32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(x), "l"(y), "l"(z));
+  return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(x), "l"(y));
+  return v;
+}
+
 // 2^e, e clamped to the normal range.
 __device__ __forceinline__ float pow2(int e) {
   e = e < -126 ? -126 : (e > 127 ? 127 : e);
@@ -686,27 +706,29 @@ __device__ __forceinline__ uint32_t many_seen(const ManyRow& r, int j, uint32_t 
   return below_hi & ~below_lo & ((there & 1u ? 0x0000ffffu : 0u) | (there & 2u ? 0xffff0000u : 0u));
 }
 
-// A tile's scores in base-2 units for a thread's row, 32 keys a step, handed
-// to `use` with their first key's number in the tile and the factors that the
-// first and the last 16 still lack.  Three forms, each a
-// rolled loop: the whole loop body of a softmax warp has to stay in the
-// instruction cache (rolled against unrolled fourfold, chunk of 4096 tokens:
-// 1,220 against 1,470 us).
-//   kPlain:  every row of the warp sees every key, no cap, no bias
+// A row's largest score over a tile, in base-2 units; lanes of .. of + 7 of
+// `ks` hold the K scales of the tile's 16-key groups (-1: not there).  Three forms:
+//   kPlain:  every row of the warp sees every key, no cap, no bias: the largest
+//            raw product of each page, times its factor
 //   kMasked: no cap, no bias
 //   kScores: everything
+// The last two put the scores themselves in the products' place, so that the
+// weights are made alike for all.  Rolled loops: what a softmax warp runs over
+// and over has to stay in the instruction cache (rolled against unrolled
+// fourfold, chunk of 4096 tokens: 1,220 against 1,470 us).
 enum ManyForm { kPlain, kMasked, kScores };
-template <ManyForm F, class Use>
-__device__ __forceinline__ void many_scores(const PagedLaunch& a, const ManyRow& r, float cap2, float ks, int j0,
-                                            uint32_t s_addr, Use use) {
+template <ManyForm F>
+__device__ __forceinline__ float many_top(const PagedLaunch& a, const ManyRow& r, float cap2, float ks, int of, int j0,
+                                          uint32_t s_addr) {
+  float top = -INFINITY;
 #pragma unroll 1
   for (int h = 0; h < 128; h += 32) {
     uint32_t x[32];
     tmem_ld(s_addr + h, x);
-    const float k0 = __shfl_sync(0xffffffffu, ks, h >> 4), k1 = __shfl_sync(0xffffffffu, ks, (h >> 4) + 1);
+    const float k0 = __shfl_sync(0xffffffffu, ks, of + (h >> 4)), k1 = __shfl_sync(0xffffffffu, ks, of + (h >> 4) + 1);
+    const float c0 = k0 * r.rf, c1 = k1 * r.rf;
     uint32_t seen = 0xffffffffu;
     if constexpr (F != kPlain) seen = many_seen(r, j0 + h, (k0 >= 0.f ? 1u : 0u) | (k1 >= 0.f ? 2u : 0u));
-    const float c0 = k0 * r.rf, c1 = k1 * r.rf;
     tmem_ld_done(x);
     if constexpr (F != kPlain) {
 #pragma unroll
@@ -718,9 +740,18 @@ __device__ __forceinline__ void many_scores(const PagedLaunch& a, const ManyRow&
         }
         x[i] = __float_as_uint(seen >> i & 1u ? v : -INFINITY);
       }
+      tmem_st_32(s_addr + h, x);
     }
-    use(h, x, F == kPlain ? c0 : 1.f, F == kPlain ? c1 : 1.f);
+    float m0 = __uint_as_float(x[0]), m1 = __uint_as_float(x[16]);
+#pragma unroll
+    for (int i = 1; i < 16; ++i) {
+      m0 = fmaxf(m0, __uint_as_float(x[i]));
+      m1 = fmaxf(m1, __uint_as_float(x[16 + i]));
+    }
+    top = fmaxf(top, F == kPlain ? fmaxf(m0 * c0, m1 * c1) : fmaxf(m0, m1));
   }
+  if constexpr (F != kPlain) tmem_st_wait();
+  return top;
 }
 
 template <int D>
@@ -995,65 +1026,49 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       }
       const bool work = keys.t0 < w.p_t1;
       if (work) {
-        // the tile's query terms, a warp per row and four rows at a time; a
-        // lane keeps the factor of its own row
+        // the tile's query terms, a thread per row: its largest magnitude (all
+        // loads in flight at once), then the codes of 16 dims at a time
         if (tile_live) {
-          constexpr int VPL = D / 32;
+          constexpr int CH = D / 8;  // 16-byte chunks of a row
+          const int tok = paged_div(a, r0 + row_in);
+          const uint4* q = reinterpret_cast<const uint4*>(
+              reinterpret_cast<const uint16_t*>(a.q) + (w.p_s.q0 + tok) * a.q_stride +
+              (int64_t)(w.p_h * a.G + r0 + row_in - tok * a.G) * D);
+          uint32_t top = 0;  // two magnitudes in bf16 bits, whose order is the numbers'
+          if (mine) {
+            uint4 u[CH];
+#pragma unroll
+            for (int i = 0; i < CH; ++i) u[i] = q[i];
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+              top = __vmaxu2(top, __vmaxu2(__vmaxu2(u[i].x & 0x7fff7fffu, u[i].y & 0x7fff7fffu),
+                                           __vmaxu2(u[i].z & 0x7fff7fffu, u[i].w & 0x7fff7fffu)));
+          }
+          const uint32_t amax = max(top & 0xffffu, top >> 16);  // from 0x7f80 on: not finite
+          const int ex = amax ? (int)(amax >> 7) - 127 - 7 : 0;
+          const float f = pow2(-ex);
+          const uint32_t dst = smem_u32(sm + C::OFF_Q + 2 * g * C::kQTerm);
 #pragma unroll 1
-          for (int i4 = 0; i4 < 32; i4 += 4) {
-            uint32_t u[4][VPL / 2];
+          for (int c = 0; c < CH; c += 2) {
+            uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+            if (mine) {
+              const uint4 u0 = q[c], u1 = q[c + 1];
+              const uint32_t wd[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int ri = (warp % 4) * 32 + i4 + q, row = r0 + ri;
-#pragma unroll
-              for (int i = 0; i < VPL / 2; ++i) u[q][i] = 0;
-              if (g * 128 + ri < rows) {
-                const int tok = paged_div(a, row);
-                const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q) + (w.p_s.q0 + tok) * a.q_stride +
-                                    (int64_t)(w.p_h * a.G + row - tok * a.G) * D + lane * VPL;
-                if constexpr (VPL == 4) {
-                  const uint2 x = *reinterpret_cast<const uint2*>(p);
-                  u[q][0] = x.x, u[q][1] = x.y;
-                } else {
-                  u[q][0] = *reinterpret_cast<const uint32_t*>(p);
-                }
-              }
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int ri = (warp % 4) * 32 + i4 + q;
-              float x[VPL], amax = 0.f;
-#pragma unroll
-              for (int i = 0; i < VPL / 2; ++i) {
-                x[2 * i] = __uint_as_float(u[q][i] << 16);
-                x[2 * i + 1] = __uint_as_float(u[q][i] & 0xffff0000u);
-              }
-#pragma unroll
-              for (int i = 0; i < VPL; ++i) amax = fmaxf(amax, fabsf(x[i]));
-              amax = warp_redux_max(amax);
-              const int ex = amax > 0.f ? (int)(__float_as_uint(amax) >> 23) - 127 - 7 : 0;
-              const float f = pow2(-ex);
-              uint32_t hi = 0, lo = 0;
-#pragma unroll
-              for (int i = 0; i < VPL / 2; ++i) {
-                const float y0 = x[2 * i] * f, y1 = x[2 * i + 1] * f;
+              for (int i = 0; i < 8; ++i) {
+                const float y0 = __uint_as_float(wd[i] << 16) * f, y1 = __uint_as_float(wd[i] & 0xffff0000u) * f;
                 const uint16_t hc = e4m3x2_code(y0, y1);
                 const float2 h = e4m3x2_val(hc);
-                hi |= (uint32_t)hc << (16 * i);
-                lo |= (uint32_t)e4m3x2_code(y0 - h.x, y1 - h.y) << (16 * i);
+                hi[i / 2] |= (uint32_t)hc << (16 * (i & 1));
+                lo[i / 2] |= (uint32_t)e4m3x2_code(y0 - h.x, y1 - h.y) << (16 * (i & 1));
               }
-              uint8_t* at = sm + C::OFF_Q + 2 * g * C::kQTerm + swz<D>(ri, lane * VPL);
-              if constexpr (VPL == 4) {
-                *reinterpret_cast<uint32_t*>(at) = hi;
-                *reinterpret_cast<uint32_t*>(at + C::kQTerm) = lo;
-              } else {
-                *reinterpret_cast<uint16_t*>(at) = (uint16_t)hi;
-                *reinterpret_cast<uint16_t*>(at + C::kQTerm) = (uint16_t)lo;
-              }
-              if (lane == i4 + q)
-                r.rf = a.sm_scale * kPagedLog2e * (amax <= 3.402823466e38f ? pow2(ex) : NAN);
             }
+            const uint32_t at = dst + swz<D>(row_in, c * 8);
+            st_shared16(at, hi[0], hi[1], hi[2], hi[3]);
+            st_shared16(at + C::kQTerm, lo[0], lo[1], lo[2], lo[3]);
           }
+          // a query that is not finite gives scores that are not numbers
+          r.rf = a.sm_scale * kPagedLog2e * (amax < 0x7f80u ? pow2(ex) : NAN);
         }
         fence_async_smem();
         __syncwarp();
@@ -1063,38 +1078,32 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       ++pieces;
       const float vref = __int_as_float(*vref_s);
       float m_ref = -INFINITY, l = 0.f;
-      // lane i < 8: the page of the tile's keys 16 i .. 16 i + 15, two tiles
-      // ahead, and its K scale one ahead
+      // Lane i holds the K scale of the keys 16 (i % 8) .. of the i / 8th of
+      // four tiles; the next four tiles' pages are looked up with these four's
+      // scales, and their scales asked for a batch ahead.
       const PageAhead<M, TK> pages(a, w, keys);
-      auto entry = [&](int t) { return pages.entry(lane < 8 ? t : INT_MAX, t * TK + lane * 16); };
+      auto entry = [&](int t) { return pages.entry(t + lane / 8, (t + lane / 8) * TK + (lane % 8) * 16); };
       if (work && tile_live) {
         const int64_t ph0 = pages.place(entry(keys.t0));
-        int32_t e1 = entry(keys.t0 + 1);
-        float ks = ph0 < 0 ? -1.f : a.k_scale[ph0];
+        int32_t e1 = entry(keys.t0 + 4);
+        float ks = -1.f, ks_next = ld_if(a.k_scale + ph0, ph0 >= 0, -1.f);
         const uint32_t prow = smem_u32(sm + C::OFF_P + g * C::kP);
         for (int t = keys.t0; t < keys.t1; ++t) {
-          const int64_t ph1 = pages.place(e1);
-          const float ks_next = ld_if(a.k_scale + ph1, ph1 >= 0, -1.f);
-          e1 = entry(t + 2);
+          const int of4 = (t - keys.t0) & 3;
+          if (of4 == 0) {
+            ks = ks_next;
+            const int64_t ph1 = pages.place(e1);
+            ks_next = ld_if(a.k_scale + ph1, ph1 >= 0, -1.f);
+            e1 = entry(t + 8);
+          }
           const int j0 = t * TK;
-          const bool inside = __all_sync(0xffffffffu, r.lo <= j0 && r.hi >= j0 + TK && (lane >= 8 || ks >= 0.f));
+          const bool inside = __all_sync(0xffffffffu, r.lo <= j0 && r.hi >= j0 + TK && (lane / 8 != of4 || ks >= 0.f));
           if (!(ok = wait(&s_full[g], (uint32_t)cnt & 1u))) break;
           tc_fence_after();
-          // the row's maximum over the tile
-          float top = -INFINITY;
-          auto maximum = [&](int, const uint32_t (&x)[32], float c0, float c1) {
-            float m0 = __uint_as_float(x[0]), m1 = __uint_as_float(x[16]);
-#pragma unroll
-            for (int i = 1; i < 16; ++i) {
-              m0 = fmaxf(m0, __uint_as_float(x[i]));
-              m1 = fmaxf(m1, __uint_as_float(x[16 + i]));
-            }
-            top = fmaxf(top, fmaxf(m0 * c0, m1 * c1));
-          };
           const ManyForm form = a.cap > 0.f || a.slopes ? kScores : inside ? kPlain : kMasked;
-          if (form == kPlain) many_scores<kPlain>(a, r, cap2, ks, j0, s_addr, maximum);
-          else if (form == kMasked) many_scores<kMasked>(a, r, cap2, ks, j0, s_addr, maximum);
-          else many_scores<kScores>(a, r, cap2, ks, j0, s_addr, maximum);
+          const float top = form == kPlain    ? many_top<kPlain>(a, r, cap2, ks, 8 * of4, j0, s_addr)
+                            : form == kMasked ? many_top<kMasked>(a, r, cap2, ks, 8 * of4, j0, s_addr)
+                                              : many_top<kScores>(a, r, cap2, ks, 8 * of4, j0, s_addr);
           const bool fresh = t == keys.t0;
           float alpha = 1.f;
           bool grown = false;
@@ -1120,35 +1129,40 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             tmem_st_wait();
           }
           const float ref = m_ref == -INFINITY ? 0.f : m_ref;
-          auto weights = [&](int h, const uint32_t (&x)[32], float c0, float c1) {
-            uint32_t pk[16];
-            float s0 = 0.f, s1 = 0.f;
+          const uint64_t ref2 = pack2(-ref, -ref);
+          uint64_t sum2 = pack2(0.f, 0.f);
+#pragma unroll 1
+          for (int h = 0; h < 128; h += 32) {
+            uint32_t x[32], pk[16];
+            tmem_ld(s_addr + h, x);
+            const float k0 = __shfl_sync(0xffffffffu, ks, 8 * of4 + (h >> 4)),
+                        k1 = __shfl_sync(0xffffffffu, ks, 8 * of4 + (h >> 4) + 1);
+            const float c0 = form == kPlain ? k0 * r.rf : 1.f, c1 = form == kPlain ? k1 * r.rf : 1.f;
+            const uint64_t c02 = pack2(c0, c0), c12 = pack2(c1, c1);
+            tmem_ld_done(x);
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-              const float c = i < 16 ? c0 : c1;
-              const float p0 = paged_ex2(fmaf(__uint_as_float(x[i]), c, -ref));
-              const float p1 = paged_ex2(fmaf(__uint_as_float(x[i + 1]), c, -ref));
-              s0 += p0;
-              s1 += p1;
+              float y0, y1;
+              unpack2(fma2(pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), i < 16 ? c02 : c12, ref2), y0, y1);
+              const float p0 = paged_ex2(y0), p1 = paged_ex2(y1);
+              sum2 = add2(sum2, pack2(p0, p1));
               const __half2 hp = __floats2half2_rn(p0, p1);
               pk[i / 2] = *reinterpret_cast<const uint32_t*>(&hp);
             }
-            l += s0 + s1;
             const uint32_t at = prow + (h >> 6) * (128 * 128);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               st_shared16(at + swz<128>(row_in, (h & 32) * 2 + i * 16), pk[4 * i], pk[4 * i + 1], pk[4 * i + 2],
                           pk[4 * i + 3]);
-          };
-          if (form == kPlain) many_scores<kPlain>(a, r, cap2, ks, j0, s_addr, weights);
-          else if (form == kMasked) many_scores<kMasked>(a, r, cap2, ks, j0, s_addr, weights);
-          else many_scores<kScores>(a, r, cap2, ks, j0, s_addr, weights);
+          }
+          float s0, s1;
+          unpack2(sum2, s0, s1);
+          l += s0 + s1;
           fence_async_smem();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full[g]);
           ++cnt;
-          ks = ks_next;
         }
         if (ok) ok = wait(&pv_done[g], (uint32_t)(cnt - 1) & 1u);
         tc_fence_after();
