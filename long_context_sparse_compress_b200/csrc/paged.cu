@@ -7,6 +7,8 @@
 // DeepSeek V4 Handles 1M Token Context" (docs.bswen.com) puts the crossover of
 // the compressed form at about 8K tokens, and the stack has a sliding-window
 // layer of its own.
+#include <type_traits>
+
 #include "kernels.cuh"
 #include "launches.h"
 #include "paged.cuh"
@@ -125,8 +127,14 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PagePlanLaunch 
       const int src = __ffs(todo) - 1;
       const int64_t n = __shfl_sync(0xffffffffu, mine, src), to = __shfl_sync(0xffffffffu, at, src);
       const int32_t* row = a.table + (int64_t)(b0 + warp * 32 + src) * a.max_blocks;
-      for (int64_t i = lane; i < n; i += 32) {
-        if (to + i < a.n_pages) a.free_pages[to + i] = row[i];
+      for (int64_t i0 = lane; i0 < n; i0 += 256) {  // eight loads in flight
+        int32_t pg[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (i0 + 32 * k < n) pg[k] = row[i0 + 32 * k];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (i0 + 32 * k < n && to + i0 + 32 * k < a.n_pages) a.free_pages[to + i0 + 32 * k] = pg[k];
       }
     }
     __syncthreads();
@@ -185,11 +193,12 @@ __global__ void __launch_bounds__(256) page_fill_kernel(PagePlanLaunch a) {
 // ------------------------------------------------------------------ store
 // A run is the adjacent tokens of one page in rising slot order: the unit of
 // work, as a page's scale needs the largest magnitude of all of them.  One CTA
-// looks at kStoreTile tokens, finds the runs that begin there and stores them
-// for one KV head of K or of V.  A run of up to kWarpRun rows is a warp's own
-// (decode steps: one row each), a longer one is shared by the CTA's warps
-// (prompts: whole pages).  Every row is read once, kept in registers between
-// the maximum and the encoding, and written once.
+// looks at TILE tokens, finds the runs that begin there and stores them for one
+// KV head of K or of V.  A run of up to kWarpRun rows is a warp's own (decode
+// steps: one row each); a longer one (prompts: whole pages) is cut into 16-byte
+// chunks that the CTA's threads share, IT for each, so that they are all in
+// flight at once and wait in IT x 4 registers for the maximum.  Every row is
+// read once and written once.
 
 constexpr int kStoreWarps = 8;
 constexpr int kWarpRun = 8;
@@ -204,11 +213,6 @@ __device__ __forceinline__ int scale_exp(float amax) {
   return s < -100 ? -100 : s;  // subnormal and zero amax: e = -127
 }
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
-
-template <int VPL>
-struct StoreRow {
-  float v[VPL];
-};
 
 // Lane's VPL values of a row; values that are not finite become 0 (and are reported).
 template <int VPL>
@@ -245,6 +249,15 @@ __device__ __forceinline__ bool store_load(const void* x, int64_t at, int dtype,
   return bad;
 }
 
+// |v|, or 0 for what is not finite.
+constexpr float kMostFinite = 3.402823466e38f;
+__device__ __forceinline__ float finite(float v, bool& bad) {
+  const float m = fabsf(v);
+  if (m <= kMostFinite) return m;
+  bad = true;
+  return 0.f;
+}
+
 template <int VPL>
 __device__ __forceinline__ float store_amax(const float (&v)[VPL]) {
   float a = 0.f;
@@ -273,10 +286,26 @@ __device__ __forceinline__ void rescale_codes(uint8_t* p, int bytes, float r, in
   }
 }
 
-template <int VPL, int TILE>
+// Values of a 16-byte chunk: eight of bf16 or four of float32.
+template <bool F32>
+__device__ __forceinline__ void chunk_values(const uint4& u, float (&v)[F32 ? 4 : 8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (F32) {
+      v[i] = __uint_as_float(w[i]);
+    } else {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+
+template <int VPL, int TILE, bool F32, int IT>
 __global__ void __launch_bounds__(kStoreWarps * 32) paged_store_kernel(PagedStoreLaunch a) {
   grid_dep_wait();
-  constexpr int D = VPL * 32;
+  constexpr int D = VPL * 32, kDt = F32 ? LCSC_DT_F32 : LCSC_DT_BF16;
+  constexpr int VPC = F32 ? 4 : 8, CPR = D / VPC;  // values of a chunk, chunks of a row
   constexpr int kLook = TILE + kMaxPage;  // a run that begins in the tile ends within these
   static_assert(kLook <= kStoreWarps * 32, "one thread per slot looked at");
   __shared__ int32_t slot_s[kLook];
@@ -344,7 +373,7 @@ __global__ void __launch_bounds__(kStoreWarps * 32) paged_store_kernel(PagedStor
 #pragma unroll
       for (int r = 0; r < kWarpRun; ++r) {
         if (r < n) {
-          bad |= store_load<VPL>(x, x0 + (i + r) * stride, a.x_dtype, v[r]);
+          bad |= store_load<VPL>(x, x0 + (i + r) * stride, kDt, v[r]);
           amax = fmaxf(amax, store_amax<VPL>(v[r]));
         }
       }
@@ -358,7 +387,7 @@ __global__ void __launch_bounds__(kStoreWarps * 32) paged_store_kernel(PagedStor
       if (lane == 0 && sc != old) scales[ph] = sc;
     }
   }
-  // long runs, the whole CTA: warp w has the rows w, w + 8, ...
+  // long runs, the whole CTA
   if (any_long) {
 #pragma unroll 1
     for (int wd = 0; wd < (TILE + 31) / 32; ++wd) {
@@ -371,14 +400,21 @@ __global__ void __launch_bounds__(kStoreWarps * 32) paged_store_kernel(PagedStor
         const int first = s & (a.page - 1);
         const int64_t ph = (int64_t)(s >> a.page_log2) * a.Hkv + h;
         const float old = first > 0 ? scales[ph] : 0.f;
-        float v[kMaxPage / kStoreWarps][VPL], amax = 0.f;
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(x) + ((t0 + i) * stride + h * D) * (F32 ? 4 : 2);
+        uint4 u[IT];
+        float amax = 0.f;
 #pragma unroll
-        for (int r = 0; r < kMaxPage / kStoreWarps; ++r) {
-          const int row = r * kStoreWarps + warp;
-          if (row < n) {
-            bad |= store_load<VPL>(x, x0 + (i + row) * stride, a.x_dtype, v[r]);
-            amax = fmaxf(amax, store_amax<VPL>(v[r]));
-          }
+        for (int k = 0; k < IT; ++k) {
+          const int c = tid + k * kStoreWarps * 32, row = c / CPR;
+          u[k] = make_uint4(0, 0, 0, 0);
+          if (row < n) u[k] = *reinterpret_cast<const uint4*>(src + row * stride * (F32 ? 4 : 2) + (c % CPR) * 16);
+        }
+#pragma unroll
+        for (int k = 0; k < IT; ++k) {
+          float v[VPC];
+          chunk_values<F32>(u[k], v);
+#pragma unroll
+          for (int q = 0; q < VPC; ++q) amax = fmaxf(amax, finite(v[q], bad));
         }
         amax = warp_max(amax);
         __syncthreads();  // the last run's maxima are read, the old scale too
@@ -392,9 +428,22 @@ __global__ void __launch_bounds__(kStoreWarps * 32) paged_store_kernel(PagedStor
         uint8_t* page = codes + (ph * a.page) * D;
         if (first > 0 && sc > old) rescale_codes(page, first * D, old * inv, tid, kStoreWarps * 32);
 #pragma unroll
-        for (int r = 0; r < kMaxPage / kStoreWarps; ++r) {
-          const int row = r * kStoreWarps + warp;
-          if (row < n) store_codes<VPL>(page + (int64_t)(first + row) * D + lane * VPL, v[r], inv);
+        for (int k = 0; k < IT; ++k) {
+          const int c = tid + k * kStoreWarps * 32, row = c / CPR;
+          if (row >= n) continue;
+          float v[VPC];
+          chunk_values<F32>(u[k], v);
+          uint32_t code[VPC / 4];
+#pragma unroll
+          for (int q = 0; q < VPC / 4; ++q) {
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = fabsf(v[4 * q + e]) <= kMostFinite ? v[4 * q + e] * inv : 0.f;
+            code[q] = e4m3x2_code(y[0], y[1]) | ((uint32_t)e4m3x2_code(y[2], y[3]) << 16);
+          }
+          uint8_t* dst = page + (int64_t)(first + row) * D + (c % CPR) * VPC;
+          if constexpr (F32) *reinterpret_cast<uint32_t*>(dst) = code[0];
+          else *reinterpret_cast<uint2*>(dst) = make_uint2(code[0], code[VPC / 4 - 1]);
         }
         if (tid == 0 && sc != old) scales[ph] = sc;
       }
@@ -654,9 +703,21 @@ cudaError_t launch_paged_store(const PagedStoreLaunch& a, cudaStream_t stream) {
   auto go = [&](auto kern, int tile) {
     return launch_pdl(kern, dim3((unsigned)((a.n_tokens + tile - 1) / tile), a.Hkv, 2), dim3(kStoreWarps * 32), 0, stream, a);
   };
-  const bool small = a.n_tokens <= 1024;
-  if (a.D == 128) return small ? go(paged_store_kernel<4, 8>, 8) : go(paged_store_kernel<4, 64>, 64);
-  return small ? go(paged_store_kernel<2, 8>, 8) : go(paged_store_kernel<2, 64>, 64);
+  const int chunks = a.page * a.D * (a.x_dtype == LCSC_DT_F32 ? 4 : 2) / 16 / (kStoreWarps * 32);  // a thread's, of a page
+  auto tile = [&](auto vpl, auto f32, auto it) {
+    constexpr int V = decltype(vpl)::value, I = decltype(it)::value;
+    constexpr bool F = decltype(f32)::value;
+    return a.n_tokens <= 1024 ? go(paged_store_kernel<V, 8, F, I>, 8) : go(paged_store_kernel<V, 64, F, I>, 64);
+  };
+  auto depth = [&](auto vpl, auto f32) {
+    return chunks <= 1   ? tile(vpl, f32, std::integral_constant<int, 1>())
+           : chunks <= 4 ? tile(vpl, f32, std::integral_constant<int, 4>())
+                         : tile(vpl, f32, std::integral_constant<int, 16>());
+  };
+  auto dtype = [&](auto vpl) {
+    return a.x_dtype == LCSC_DT_F32 ? depth(vpl, std::true_type()) : depth(vpl, std::false_type());
+  };
+  return a.D == 128 ? dtype(std::integral_constant<int, 4>()) : dtype(std::integral_constant<int, 2>());
 }
 
 PagedForm paged_form(int q_dtype, int D, int G, int64_t max_new) {

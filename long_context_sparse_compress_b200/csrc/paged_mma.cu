@@ -683,8 +683,9 @@ struct ManyCfg {
   static constexpr int OFF_V = OFF_K + 2 * kK;        // [2]
   static constexpr int OFF_P = OFF_V + 2 * kV;        // [2 tiles]
   static constexpr int OFF_BAR = OFF_P + 2 * kP;
-  static constexpr int kBars = 18;
-  static constexpr int OFF_SCAN = OFF_BAR + kBars * 8;  // PagedScratch
+  static constexpr int kBars = 19;
+  static constexpr int OFF_ML = OFF_BAR + (kBars + 1) / 2 * 16;  // float2 [128]: the second warpgroup's maxima and sums
+  static constexpr int OFF_SCAN = OFF_ML + 128 * 8;  // PagedScratch
   static constexpr int OFF_VREF = OFF_SCAN + (int)sizeof(PagedScratch);    // int: largest V scale of the piece (bits)
   static constexpr int OFF_TM = OFF_VREF + 4;
   static constexpr int OFF_ABORT = OFF_TM + 4;
@@ -773,6 +774,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   uint64_t* ref_full = k_full + 15;  // the piece's largest V scale
   uint64_t* piece_done = k_full + 16;
   uint64_t* drain = k_full + 17;
+  uint64_t* ml_full = k_full + 18;   // the second warpgroup's part of a shared block of rows
+  float2* ml_s = reinterpret_cast<float2*>(sm + C::OFF_ML);
   volatile int* vref_s = reinterpret_cast<volatile int*>(sm + C::OFF_VREF);
   uint32_t* tm_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_TM);
   volatile int* abort = reinterpret_cast<volatile int*>(sm + C::OFF_ABORT);
@@ -789,6 +792,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     mbar_init(ref_full, 4);
     mbar_init(piece_done, 8);
     mbar_init(drain, 1);
+    mbar_init(ml_full, 4);
     *abort = 0;
     fence_barrier_init();
   }
@@ -842,57 +846,56 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const uint32_t qa = smem_u32(sm + C::OFF_Q);
     bool go = !test.stall || wait(drain, 0);  // a test of the failure path: nothing has committed to it yet
     int n = 0, pieces = 0, cnt[2] = {0, 0};
-    auto issue_pv = [&](int g, bool last, bool acc) {  // P V of tile n - 1 (its P and V are there)
-      if (elect_one()) {
-        const int b = (n - 1) & 1;
-        const uint32_t pa = smem_u32(sm + C::OFF_P + g * C::kP), va = smem_u32(sm + C::OFF_V + b * C::kV);
-#pragma unroll
-        for (int k = 0; k < TK / 16; ++k)
-          mma_ss<0>(tmem + 256 + g * 128, smem_desc(pa + (k / 4) * (128 * 128) + (k % 4) * 32, 16, 1024, kSw128),
-                    smem_desc(va + k * 16 * 128, TK * 128, 1024, kSw128), idesc_pv, acc || k > 0);
-        tc_commit(&pv_done[g]);
-        if (last) tc_commit(&v_empty[b]);
-      }
-      __syncwarp();
-    };
     while (go && w.next()) {
       const PieceKeys<M, TK> keys(a, w);
       if (keys.t0 >= w.p_t1) continue;
-      const int tiles = w.rows() > 128 ? 2 : 1;
+      const bool shared = w.rows() <= 128;  // both warpgroups on one tile of rows
       if (!(go = wait(q_full, (uint32_t)pieces & 1u))) break;
       ++pieces;
-      for (int t = keys.t0; go && t < keys.t1; ++t) {
+      const int T = keys.t1 - keys.t0, last = shared ? 0 : 1;
+      // Per tile of keys: Q K^T of the next, P V of the last, for each tile of
+      // rows or, where there is one, for the warpgroups in turn.
+      for (int i = 0; go && i <= T; ++i) {
         const int s = n & 1;
-        if (!(go = wait(&k_full[s], (uint32_t)(n >> 1) & 1u))) break;
-        for (int g = 0; g < tiles; ++g) {
-          if (t > keys.t0 && !(go = wait(&p_full[g], (uint32_t)(cnt[g] - 1) & 1u))) break;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t ka = smem_u32(sm + C::OFF_K + s * C::kK);
-#pragma unroll
-            for (int term = 0; term < kQTerms; ++term)
-#pragma unroll
-              for (int k = 0; k < D / 32; ++k)
-                mma_ss<1>(tmem + g * 128, smem_desc(qa + (2 * g + term) * C::kQTerm + k * 32, 16, 8 * D, kSwOf<D>),
-                          smem_desc(ka + k * 32, 16, 8 * D, kSwOf<D>), idesc_qk, k > 0 || term > 0);
-            tc_commit(&s_full[g]);
-            if (g == tiles - 1) tc_commit(&k_empty[s]);
-          }
-          __syncwarp();
-          ++cnt[g];
-          if (t > keys.t0) {
-            if (g == 0 && !(go = wait(&v_full[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u))) break;
+        if (i < T && !(go = wait(&k_full[s], (uint32_t)(n >> 1) & 1u))) break;
+        for (int e = 0; e <= last; ++e) {
+          const int gq = shared ? i & 1 : e, gp = shared ? gq ^ 1 : e;
+          if (!shared && i > 0 && !(go = wait(&p_full[gp], (uint32_t)(cnt[gp] - 1) & 1u))) break;
+          if (i < T) {
             tc_fence_after();
-            issue_pv(g, g == tiles - 1, t - 1 > keys.t0);
+            if (elect_one()) {
+              const uint32_t ka = smem_u32(sm + C::OFF_K + s * C::kK), qt = qa + (shared ? 0 : 2 * e) * C::kQTerm;
+#pragma unroll
+              for (int term = 0; term < kQTerms; ++term)
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k)
+                  mma_ss<1>(tmem + gq * 128, smem_desc(qt + term * C::kQTerm + k * 32, 16, 8 * D, kSwOf<D>),
+                            smem_desc(ka + k * 32, 16, 8 * D, kSwOf<D>), idesc_qk, k > 0 || term > 0);
+              tc_commit(&s_full[gq]);
+              if (e == last) tc_commit(&k_empty[s]);
+            }
+            __syncwarp();
           }
+          if (i > 0) {
+            const int m = n - 1, b = m & 1;
+            if (shared && !(go = wait(&p_full[gp], (uint32_t)(cnt[gp] - 1) & 1u))) break;
+            if (e == 0 && !(go = wait(&v_full[b], (uint32_t)(m >> 1) & 1u))) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t pa = smem_u32(sm + C::OFF_P + gp * C::kP), va = smem_u32(sm + C::OFF_V + b * C::kV);
+              const bool acc = i > (shared ? 2 : 1);
+#pragma unroll
+              for (int k = 0; k < TK / 16; ++k)
+                mma_ss<0>(tmem + 256 + gp * 128, smem_desc(pa + (k / 4) * (128 * 128) + (k % 4) * 32, 16, 1024, kSw128),
+                          smem_desc(va + k * 16 * 128, TK * 128, 1024, kSw128), idesc_pv, acc || k > 0);
+              tc_commit(&pv_done[gp]);
+              if (e == last) tc_commit(&v_empty[b]);
+            }
+            __syncwarp();
+          }
+          if (i < T) ++cnt[gq];
         }
-        if (go) ++n;
-      }
-      for (int g = 0; go && g < tiles; ++g) {
-        if (!(go = wait(&p_full[g], (uint32_t)(cnt[g] - 1) & 1u))) break;
-        if (g == 0 && !(go = wait(&v_full[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u))) break;
-        tc_fence_after();
-        issue_pv(g, g == tiles - 1, w.p_t1 - 1 > keys.t0);
+        if (go && i < T) ++n;
       }
     }
     if (lane == 0) {
@@ -1009,13 +1012,17 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const uint32_t lane_base = (uint32_t)((warp % 4) * 32) << 16;
     const uint32_t s_addr = tmem + g * 128 + lane_base, o_addr = tmem + 256 + g * 128 + lane_base;
     bool ok = true, first = true;
-    int cnt = 0, pieces = 0;
+    int cnt = 0, pieces = 0, merges = 0;
     while (ok && w.next()) {
       if (tid == 0 && first) w.write_meta(false);
       first = false;
       const PieceKeys<M, TK> keys(a, w);
-      const int rows = w.rows(), r0 = w.p_mt * M + g * 128;
-      const bool mine = g * 128 + row_in < rows, tile_live = g * 128 < rows;
+      const int rows = w.rows();
+      // Up to 128 rows are one tile that both warpgroups work on, taking its
+      // tiles of keys in turn, each with its own maxima, sums and O.
+      const bool shared = rows <= 128;
+      const int r_in = (shared ? 0 : g * 128) + row_in, r0 = w.p_mt * M + r_in - row_in;
+      const bool mine = r_in < rows;
       ManyRow r = {0, INT_MAX, 0, 0.f, 0.f};
       if (mine) {
         const int i = paged_div(a, r0 + row_in);
@@ -1028,7 +1035,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       if (work) {
         // the tile's query terms, a thread per row: its largest magnitude (all
         // loads in flight at once), then the codes of 16 dims at a time
-        if (tile_live) {
+        {
           constexpr int CH = D / 8;  // 16-byte chunks of a row
           const int tok = paged_div(a, r0 + row_in);
           const uint4* q = reinterpret_cast<const uint4*>(
@@ -1064,6 +1071,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
               }
             }
             const uint32_t at = dst + swz<D>(row_in, c * 8);
+            if (shared && g == 1) continue;  // the first warpgroup lays them out
             st_shared16(at, hi[0], hi[1], hi[2], hi[3]);
             st_shared16(at + C::kQTerm, lo[0], lo[1], lo[2], lo[3]);
           }
@@ -1083,18 +1091,19 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       // scales, and their scales asked for a batch ahead.
       const PageAhead<M, TK> pages(a, w, keys);
       auto entry = [&](int t) { return pages.entry(t + lane / 8, (t + lane / 8) * TK + (lane % 8) * 16); };
-      if (work && tile_live) {
+      if (work) {
         const int64_t ph0 = pages.place(entry(keys.t0));
         int32_t e1 = entry(keys.t0 + 4);
         float ks = -1.f, ks_next = ld_if(a.k_scale + ph0, ph0 >= 0, -1.f);
         const uint32_t prow = smem_u32(sm + C::OFF_P + g * C::kP);
-        for (int t = keys.t0; t < keys.t1; ++t) {
+        const int t_first = keys.t0 + (shared ? g : 0), t_step = shared ? 2 : 1;
+        for (int t = t_first; t < keys.t1; t += t_step) {
           const int of4 = (t - keys.t0) & 3;
-          if (of4 == 0) {
+          if (of4 < t_step) {  // the first of four tiles, or of this warpgroup's two of them
             ks = ks_next;
             const int64_t ph1 = pages.place(e1);
             ks_next = ld_if(a.k_scale + ph1, ph1 >= 0, -1.f);
-            e1 = entry(t + 8);
+            e1 = entry(t - of4 + 8);
           }
           const int j0 = t * TK;
           const bool inside = __all_sync(0xffffffffu, r.lo <= j0 && r.hi >= j0 + TK && (lane / 8 != of4 || ks >= 0.f));
@@ -1104,7 +1113,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           const float top = form == kPlain    ? many_top<kPlain>(a, r, cap2, ks, 8 * of4, j0, s_addr)
                             : form == kMasked ? many_top<kMasked>(a, r, cap2, ks, 8 * of4, j0, s_addr)
                                               : many_top<kScores>(a, r, cap2, ks, 8 * of4, j0, s_addr);
-          const bool fresh = t == keys.t0;
+          const bool fresh = t == t_first;
           float alpha = 1.f;
           bool grown = false;
           if (top > m_ref + kLazy || (fresh && top > -INFINITY)) {
@@ -1164,17 +1173,36 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           if (lane == 0) mbar_arrive(&p_full[g]);
           ++cnt;
         }
-        if (ok) ok = wait(&pv_done[g], (uint32_t)(cnt - 1) & 1u);
+        if (ok && t_first < keys.t1) ok = wait(&pv_done[g], (uint32_t)(cnt - 1) & 1u);
         tc_fence_after();
       }
       if (!ok) break;
+      float f_own = 1.f, f_other = 0.f;  // of O in this warpgroup's and the other's columns
+      if (shared && work) {
+        if (g == 1) {
+          ml_s[row_in] = make_float2(m_ref, l);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ml_full);
+        } else {
+          if (!(ok = wait(ml_full, (uint32_t)merges & 1u))) break;
+          tc_fence_after();
+          const float2 o = ml_s[row_in];
+          const float m = fmaxf(m_ref, o.x), ref = m == -INFINITY ? 0.f : m;
+          f_own = paged_ex2(m_ref - ref);
+          f_other = paged_ex2(o.x - ref);
+          l = fmaf(l, f_own, o.y * f_other);
+          m_ref = m;
+        }
+        ++merges;
+      }
       // O (times 2^7 / vref), the row's maximum and sum
-      if (tile_live) {
+      if (!(shared && g == 1)) {
         const float unit = vref * (1.f / 128.f);
         const int row = r0 + row_in;
         const int tok = paged_div(a, row), head = w.p_h * a.G + row - tok * a.G;
         const int64_t at = (w.p_s.q0 + tok) * a.Hq + head;
-        const int64_t part = w.slot() * M + g * 128 + row_in;
+        const int64_t part = w.slot() * M + r_in;
         float f = unit;
         if (w.whole()) {
           float top = m_ref, den = l;
@@ -1199,6 +1227,14 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           if (work) {
             tmem_ld(o_addr + d, o);
             tmem_ld_done(o);
+          }
+          if (shared && keys.t0 + 1 < keys.t1) {  // the other warpgroup had keys
+            uint32_t x[32];
+            tmem_ld(o_addr + 128 + d, x);
+            tmem_ld_done(x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              o[i] = __float_as_uint(fmaf(__uint_as_float(o[i]), f_own, __uint_as_float(x[i]) * f_other));
           }
           if (!mine) continue;
 #pragma unroll
@@ -1293,7 +1329,7 @@ cudaError_t launch_mma(const PagedLaunch& a, const PagedForm& f, const CUtensorM
 
 PagedForm paged_mma_form(int D, int G, int64_t max_new) {
   const int64_t rows = max_new * G;
-  if (rows > 64) return {2, kManyRows, sm_count()};
+  if (rows > 16) return {2, kManyRows, sm_count()};
   return {1, rows <= 8 ? 8 : rows <= 16 ? 16 : 32, 2 * sm_count()};
 }
 

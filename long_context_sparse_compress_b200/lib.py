@@ -448,46 +448,68 @@ class PagedCache:
         for x in (k_scale, v_scale):
             if x.shape != k.shape[:2] or x.dtype != torch.float32 or not x.is_contiguous():
                 raise LcscError("page scales: two contiguous float32 tensors [n_pages][n_kv_heads]")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.n_pages = k.shape[0]
+        self._tensors = (k, v, k_scale, v_scale)
+        self.n_pages, *self.page = k.shape
+        self.device = {x.get_device() for x in self._tensors}
+        self._c = PagedPool(*(x.data_ptr() for x in self._tensors), self.n_pages)
+
+    # the tensors are the cache's for good: the struct of the calls points to them
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_scale = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
 
     def c(self):
-        return PagedPool(k=self.k.data_ptr(), v=self.v.data_ptr(), k_scale=self.k_scale.data_ptr(),
-                         v_scale=self.v_scale.data_ptr(), n_pages=self.n_pages)
+        return self._c
 
 
-def _on_device(stream, *tensors):
-    """Every tensor (None: absent) lies on the current device, where the kernels are launched."""
-    dev = {t.get_device() for t in tensors if t is not None}
-    if stream is not None:
-        dev.add(stream.device_index)
-    if len(dev) != 1 or -1 in dev or dev.pop() != torch.cuda.current_device():
+class _Args:
+    """Checks the tensors of one paged call and hands out their pointers: all
+    on one device, which is the current one when the call is made."""
+
+    def __init__(self, stream, cache=None):
+        self.stream = stream
+        self.devices = set() if cache is None else set(cache.device)
+
+    def dense(self, name, t, dtype, n=None):
+        """A contiguous array of n values (None: absent)."""
+        if t is None:
+            return None
+        if t.dtype is not dtype or not t.is_contiguous() or (n is not None and t.numel() != n):
+            raise LcscError(f"{name}: a contiguous {dtype} tensor" + ("" if n is None else f" of {n} values"))
+        self.devices.add(t.get_device())
+        return t.data_ptr()
+
+    def rows(self, name, t, heads, head_dim, dtype):
+        """Pointer and row stride (values) of a [tokens][heads][head_dim] view whose rows are dense."""
+        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim or t.dtype is not dtype:
+            raise LcscError(f"{name}: [tokens][{heads}][{head_dim}] of {dtype}")
+        stride, across, along = t.stride()
+        if t.shape[0] and (along != 1 or (heads > 1 and across != head_dim)):
+            raise LcscError(f"{name}: the values of a token's heads must be adjacent")
+        self.devices.add(t.get_device())
+        return t.data_ptr(), (stride if t.shape[0] > 1 else heads * head_dim)
+
+    def handle(self):
+        """The stream, once every tensor is known to be on the current device."""
+        s = self.stream
+        if s is not None:
+            self.devices.add(s.device_index)
+        if len(self.devices) == 1 and -1 not in self.devices:
+            dev = self.devices.pop()
+            if dev == torch.cuda.current_device():
+                return (torch.cuda.current_stream(dev) if s is None else s).cuda_stream
         raise LcscError("every tensor and the stream must be on the current CUDA device")
 
 
-def _i32(name, t, n=None):
-    """An int32 array that the paged calls read or write densely."""
-    if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or (n is not None and t.numel() != n)):
-        raise LcscError(f"{name}: a contiguous int32 tensor" + ("" if n is None else f" of {n} values"))
-    return ptr(t)
-
-
-def _token_rows(name, t, heads, head_dim, dtype):
-    """Pointer and row stride (values) of a [tokens][heads][head_dim] view whose rows are dense."""
-    if t.dim() != 3 or t.shape[1:] != (heads, head_dim) or t.dtype != dtype:
-        raise LcscError(f"{name}: [tokens][{heads}][{head_dim}] of {dtype}")
-    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim)):
-        raise LcscError(f"{name}: the values of a token's heads must be adjacent")
-    return ptr(t), (t.stride(0) if t.shape[0] > 1 else heads * head_dim)
-
-
 _TORCH_DT = {0: torch.float32, 1: torch.bfloat16}
+_I32, _F32 = torch.int32, torch.float32
 
 
 def _pool_of(p, cache):
-    if tuple(cache.k.shape[1:]) != (p.n_kv_heads, p.page_size, p.head_dim):
-        raise LcscError(f"cache pages {tuple(cache.k.shape[1:])} are not the parameters' "
-                        f"({p.n_kv_heads}, {p.page_size}, {p.head_dim})")
+    if cache.page != [p.n_kv_heads, p.page_size, p.head_dim]:
+        raise LcscError(f"cache pages {cache.page} are not the parameters' "
+                        f"{[p.n_kv_heads, p.page_size, p.head_dim]}")
     return cache.c()
 
 
@@ -499,35 +521,34 @@ def page_plan(page_size, cached, n_new, block_table, free_pages, n_free, n_free_
               positions=None, ws=None, status=None, stream=None):
     """lcsc_page_plan: lengths, first rows, slots and block-table entries of a
     serving step from the requests' cached and new token counts."""
-    B = cached.numel()
+    B, n, arg = cached.numel(), slots.numel(), _Args(stream)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise LcscError(f"block_table: [{B}][max_blocks]")
-    _on_device(stream, cached, n_new, block_table, free_pages, n_free, n_free_out, ctx_len, q_start, slots, positions,
-               ws, status)
+    ints = [arg.dense(name, t, _I32, size) for name, t, size in (
+        ("cached", cached, B), ("n_new", n_new, B), ("block_table", block_table, None),
+        ("free_pages", free_pages, None), ("n_free", n_free, 1), ("n_free_out", n_free_out, 1),
+        ("ctx_len", ctx_len, B), ("q_start", q_start, B + 1), ("slots", slots, n), ("positions", positions, n))]
+    st, handle = arg.dense("status", status, _I32), None
     if ws is None:
+        handle = arg.handle()
         ws = workspace(page_plan_workspace(B), cached.device)
-    n = slots.numel()
-    check(load().lcsc_page_plan(
-        page_size, B, n, block_table.shape[1], free_pages.numel(), _i32("cached", cached, B),
-        _i32("n_new", n_new, B), _i32("block_table", block_table), _i32("free_pages", free_pages),
-        _i32("n_free", n_free, 1), _i32("n_free_out", n_free_out, 1), _i32("ctx_len", ctx_len, B),
-        _i32("q_start", q_start, B + 1), _i32("slots", slots), _i32("positions", positions, n), ptr(ws), ws.numel(),
-        ptr(status), stream_handle(stream)))
+    wp = arg.dense("ws", ws, torch.uint8)
+    check(load().lcsc_page_plan(page_size, B, n, block_table.shape[1], free_pages.numel(), *ints, wp, ws.numel(), st,
+                                handle or arg.handle()))
     return ws
 
 
 def paged_store(p, cache, k, v, slots, status=None, stream=None):
     """lcsc_paged_store: K and V rows [tokens][n_kv_heads][head_dim] (the
     token stride is free) into their slots."""
-    pool = _pool_of(p, cache)
-    n = slots.numel()
-    kp, ks = _token_rows("k", k, p.n_kv_heads, p.head_dim, _TORCH_DT[p.x_dtype])
-    vp, vs = _token_rows("v", v, p.n_kv_heads, p.head_dim, _TORCH_DT[p.x_dtype])
+    pool, arg = _pool_of(p, cache), _Args(stream, cache)
+    n, heads, dim, dtype = slots.numel(), p.n_kv_heads, p.head_dim, _TORCH_DT[p.x_dtype]
+    kp, ks = arg.rows("k", k, heads, dim, dtype)
+    vp, vs = arg.rows("v", v, heads, dim, dtype)
     if k.shape[0] != n or v.shape[0] != n:
         raise LcscError(f"k and v: a row for each of the {n} slots")
-    _on_device(stream, cache.k, cache.v, cache.k_scale, cache.v_scale, k, v, slots, status)
-    check(load().lcsc_paged_store(ctypes.byref(p), ctypes.byref(pool), kp, ks, vp, vs, _i32("slots", slots), n,
-                                  ptr(status), stream_handle(stream)))
+    sp, st = arg.dense("slots", slots, _I32), arg.dense("status", status, _I32)
+    check(load().lcsc_paged_store(ctypes.byref(p), ctypes.byref(pool), kp, ks, vp, vs, sp, n, st, arg.handle()))
 
 
 def paged_attn_workspace(p, B, n_tokens, max_new):
@@ -538,28 +559,25 @@ def paged_attn(p, q, cache, block_table, ctx_len, q_start, max_new, out, lse=Non
                prefix_len=None, doc_start=None, ws=None, status=None, stream=None):
     """lcsc_paged_attn: queries [tokens][n_heads][head_dim] (the token stride
     is free) over the cached tokens of their requests."""
-    pool = _pool_of(p, cache)
-    n, B = q.shape[0], ctx_len.numel()
-    qp, qs = _token_rows("q", q, p.n_heads, p.head_dim, _TORCH_DT[p.q_dtype])
-    if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
-        raise LcscError("out: contiguous, of q's shape and type")
+    pool, arg = _pool_of(p, cache), _Args(stream, cache)
+    n, B, heads, dense = q.shape[0], ctx_len.numel(), p.n_heads, arg.dense
+    qp, qs = arg.rows("q", q, heads, p.head_dim, _TORCH_DT[p.q_dtype])
+    if out.shape != q.shape:
+        raise LcscError("out: of q's shape")
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise LcscError(f"block_table: [{B}][max_blocks]")
-    for name, t, size in (("lse", lse, n * p.n_heads), ("slopes", slopes, p.n_heads), ("sink", sink, p.n_heads)):
-        if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != size):
-            raise LcscError(f"{name}: a contiguous float32 tensor of {size} values")
-    _on_device(stream, cache.k, cache.v, cache.k_scale, cache.v_scale, q, block_table, ctx_len, q_start, out, lse,
-               slopes, sink, prefix_len, doc_start, ws, status)
+    batch = PagedBatch(
+        B, n, max_new, block_table.shape[1], dense("q_start", q_start, _I32, B + 1), dense("ctx_len", ctx_len, _I32),
+        dense("block_table", block_table, _I32), qp, qs, dense("out", out, q.dtype),
+        dense("lse", lse, _F32, n * heads), dense("slopes", slopes, _F32, heads), dense("sink", sink, _F32, heads),
+        dense("prefix_len", prefix_len, _I32, B), dense("doc_start", doc_start, _I32, n))
+    st, handle = dense("status", status, _I32), None
     if ws is None:
+        handle = arg.handle()
         ws = workspace(paged_attn_workspace(p, B, n, max_new), q.device)
-    batch = PagedBatch(B=B, n_tokens=n, max_new=max_new, max_blocks=block_table.shape[1], q_stride=qs)
-    for name, t in dict(q_start=_i32("q_start", q_start, B + 1), ctx_len=_i32("ctx_len", ctx_len),
-                        block_table=_i32("block_table", block_table), q=qp, out=ptr(out), lse=ptr(lse),
-                        slopes=ptr(slopes), sink=ptr(sink), prefix_len=_i32("prefix_len", prefix_len, B),
-                        doc_start=_i32("doc_start", doc_start, n)).items():
-        setattr(batch, name, t)
-    check(load().lcsc_paged_attn(ctypes.byref(p), ctypes.byref(batch), ctypes.byref(pool), ptr(ws), ws.numel(),
-                                 ptr(status), stream_handle(stream)))
+    wp = dense("ws", ws, torch.uint8)
+    check(load().lcsc_paged_attn(ctypes.byref(p), ctypes.byref(batch), ctypes.byref(pool), wp, ws.numel(), st,
+                                 handle or arg.handle()))
     return ws
 
 
