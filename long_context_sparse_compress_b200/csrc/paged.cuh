@@ -180,19 +180,15 @@ __device__ __forceinline__ int64_t paged_warp_sum(int64_t v) {
   return v;
 }
 
-// Units of a request's head, by a whole warp (the same request in every lane).
-template <int M, int TK>
-__device__ __forceinline__ int64_t paged_units_warp(const PagedLaunch& a, int b) {
-  const PagedSeq s = paged_seq(a, b);
-  const int prefix = paged_prefix(a, b);
-  int64_t u = 0;
-  for (int mt = threadIdx.x & 31; (int64_t)mt * M < (int64_t)s.n * a.G; mt += 32)
-    u += paged_tile_count<M, TK>(a, s, prefix, mt);
-  return paged_warp_sum(u);
+// Quotient of two numbers that fit 32 bits nearly always (a 64-bit division is a
+// long piece of code, and code that runs once is paid for in instruction fetches).
+__device__ __forceinline__ int64_t paged_quot(int64_t x, int64_t y) {
+  if (((x | y) >> 32) == 0) return (int64_t)((uint32_t)x / (uint32_t)y);
+  return x / y;
 }
 
-// Units of request b, one request per lane (a.B: none): those of few row
-// blocks by their lane, the others by the warp together.
+// Units of a head of request b, one request per lane (a.B: none): those of few
+// row blocks by their lane, the others by the warp together.
 template <int M, int TK>
 __device__ __forceinline__ int64_t paged_units(const PagedLaunch& a, int b) {
   PagedSeq s = {0, 0, 0};
@@ -200,22 +196,34 @@ __device__ __forceinline__ int64_t paged_units(const PagedLaunch& a, int b) {
   const int prefix = b < a.B ? paged_prefix(a, b) : 0;
   const bool few = (int64_t)s.n * a.G <= 4 * M;
   int64_t u = 0;
-  if (few)
+  if (few) {
+#pragma unroll 1
     for (int mt = 0; mt < 4; ++mt) u += paged_tile_count<M, TK>(a, s, prefix, mt);
+  }
+#pragma unroll 1
   for (unsigned todo = __ballot_sync(0xffffffffu, !few); todo; todo &= todo - 1) {
-    const int src = __ffs(todo) - 1;
-    const int64_t sum = paged_units_warp<M, TK>(a, __shfl_sync(0xffffffffu, b, src));
+    const int src = __ffs(todo) - 1, bs = __shfl_sync(0xffffffffu, b, src);
+    const PagedSeq t = paged_seq(a, bs);
+    const int pre = paged_prefix(a, bs);
+    int64_t sum = 0;
+#pragma unroll 1
+    for (int mt = threadIdx.x & 31; (int64_t)mt * M < (int64_t)t.n * a.G; mt += 32)
+      sum += paged_tile_count<M, TK>(a, t, pre, mt);
+    sum = paged_warp_sum(sum);
     if ((int)(threadIdx.x & 31) == src) u = sum;
   }
-  return u * a.Hkv;
+  return u;
 }
 
-// CTA c of `ctas` that have work (no more of them than units).
+// The units' shares of the CTAs that have work: the first total % ctas have one more.
 struct PagedShare {
-  int64_t total;
-  int ctas;
-  __device__ __forceinline__ int64_t begin(int c) const { return total * c / ctas; }
-  __device__ __forceinline__ int owner(int64_t u) const { return (int)(((u + 1) * ctas - 1) / total); }
+  int64_t total, each;  // units of the call, units of a CTA (the fewer)
+  int ctas, more;       // CTAs with work, CTAs with one unit more
+  __device__ __forceinline__ int64_t begin(int c) const { return c * each + min(c, more); }
+  __device__ __forceinline__ int owner(int64_t u) const {
+    const int64_t high = (each + 1) * more;
+    return u < high ? (int)paged_quot(u, each + 1) : more + (int)paged_quot(u - high, each);
+  }
 };
 
 // Where a CTA's share begins: found once by the whole CTA.
@@ -223,8 +231,8 @@ struct PagedStart {
   int b, h, mt, t;  // b = -1: no share
 };
 struct PagedScratch {
-  int64_t scan[33];  // sums of the warps; [32]: of the CTA
-  int64_t first;     // units before the found request
+  int64_t scan[33];         // sums of the warps; [32]: of the CTA
+  int64_t first, per_head;  // units before the found request, and of one of its heads
   PagedStart st;
 };
 
@@ -232,74 +240,81 @@ struct PagedScratch {
 template <int M, int TK>
 __device__ __forceinline__ PagedStart paged_start(const PagedLaunch& a, PagedShare* share, PagedScratch* x) {
   const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nthr >> 5;
-  auto inclusive = [&](int64_t v) {  // over the CTA's threads; scan[32]: their sum
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t w = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += w;
-    }
-    __syncthreads();
-    if (lane == 31) x->scan[warp] = v;
-    __syncthreads();
-    int64_t before = 0, all = 0;
-    for (int w = 0; w < warps; ++w) {
-      const int64_t y = x->scan[w];
-      if (w < warp) before += y;
-      all += y;
-    }
-    if (tid == 0) x->scan[32] = all;
-    __syncthreads();
-    return v + before;
-  };
   if (tid == 0) x->st.b = -1;
-  int64_t total = 0;
-  for (int b0 = 0; b0 < a.B; b0 += nthr) {
-    inclusive(paged_units<M, TK>(a, b0 + tid < a.B ? b0 + tid : a.B));
-    total += x->scan[32];
-  }
-  share->total = total;
-  share->ctas = (int)min((int64_t)gridDim.x, total);
-  if ((int)blockIdx.x < share->ctas) {  // the same for the whole CTA
-    const int64_t u0 = share->begin(blockIdx.x);
+  int64_t u0 = 0, u = 0;
+  // first for the sum over all requests, then for the one the share begins in
+#pragma unroll 1
+  for (int find = 0; find < 2; ++find) {
     int64_t base = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < a.B; b0 += nthr) {
       const int b = b0 + tid;
-      const int64_t u = paged_units<M, TK>(a, b < a.B ? b : a.B);
-      const int64_t end = base + inclusive(u);
-      if (end - u <= u0 && u0 < end) {  // one thread at most
-        x->st.b = b;
-        x->first = end - u;
-      }
-      base += x->scan[32];
-      if (base > u0) break;
-    }
-    __syncthreads();
-    if (warp == 0) {  // the head, row block and tile
-      const int b = x->st.b;
-      const PagedSeq s = paged_seq(a, b);
-      const int prefix = paged_prefix(a, b);
-      const int64_t per_head = paged_units_warp<M, TK>(a, b);
-      int64_t off = (u0 - x->first) % per_head;
-      const int h = (int)((u0 - x->first) / per_head);
-      for (int m0 = 0;; m0 += 32) {
-        const int c = paged_tile_count<M, TK>(a, s, prefix, m0 + lane);
-        int64_t upto = c;
+      if (!find || a.B > nthr) u = paged_units<M, TK>(a, b < a.B ? b : a.B);
+      int64_t upto = u * a.Hkv;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += y;
-        }
-        const bool here = upto - c <= off && off < upto;
-        if (here) {
-          int t0, t1;
-          paged_tiles<M, TK>(a, s, prefix, m0 + lane, &t0, &t1);
-          x->st.h = h;
-          x->st.mt = m0 + lane;
-          x->st.t = t0 + (int)(off - (upto - c));
-        }
-        if (__any_sync(0xffffffffu, here)) break;
-        off -= __shfl_sync(0xffffffffu, upto, 31);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
       }
+      __syncthreads();
+      if (lane == 31) x->scan[warp] = upto;
+      __syncthreads();
+      int64_t all = 0;
+#pragma unroll 1
+      for (int i = 0; i < warps; ++i) {
+        const int64_t y = x->scan[i];
+        if (i < warp) upto += y;
+        all += y;
+      }
+      upto += base;
+      if (find && upto - u * a.Hkv <= u0 && u0 < upto) {  // one thread at most
+        x->st.b = b;
+        x->first = upto - u * a.Hkv;
+        x->per_head = u;
+      }
+      base += all;
+      if (find && base > u0) break;  // the same for the whole CTA
+    }
+    if (!find) {
+      // At least two tiles for a CTA of few rows (decode of 16 requests with a
+      // window of 128: 19.7 against 23.4 us with one, 28.1 with three), one of
+      // many rows (a prompt of 400 tokens: 42.6 against 55.6 us with two).
+      constexpr int kLeast = M > 64 ? 1 : 2;
+      share->total = base;
+      share->ctas = (int)min((int64_t)gridDim.x, (base + kLeast - 1) / kLeast);
+      if ((int)blockIdx.x >= share->ctas) break;  // the same for the whole CTA
+      share->each = paged_quot(base, share->ctas);
+      share->more = (int)(base - share->each * share->ctas);
+      u0 = share->begin(blockIdx.x);
+    }
+  }
+  __syncthreads();
+  if (warp == 0 && x->st.b >= 0) {  // the head, row block and tile
+    const int b = x->st.b;
+    const PagedSeq s = paged_seq(a, b);
+    const int prefix = paged_prefix(a, b);
+    int64_t off = u0 - x->first;
+    const int h = (int)paged_quot(off, x->per_head);
+    off -= h * x->per_head;
+#pragma unroll 1
+    for (int m0 = 0;; m0 += 32) {
+      const int c = paged_tile_count<M, TK>(a, s, prefix, m0 + lane);
+      int64_t upto = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const bool here = upto - c <= off && off < upto;
+      if (here) {
+        int t0, t1;
+        paged_tiles<M, TK>(a, s, prefix, m0 + lane, &t0, &t1);
+        x->st.h = h;
+        x->st.mt = m0 + lane;
+        x->st.t = t0 + (int)(off - (upto - c));
+      }
+      if (__any_sync(0xffffffffu, here)) break;
+      off -= __shfl_sync(0xffffffffu, upto, 31);
     }
   }
   __syncthreads();

@@ -324,8 +324,10 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
     constexpr int kMaxPages = TK / 16;
     const int per = TK >> a.page_log2;  // pages of a tile
     const uint32_t page_bytes = (uint32_t)a.page * D;
-    bool go = true;
+    bool go = true, first = true;
     while (go && w.next()) {
+      if (lane == 0 && first) w.write_meta(false);
+      first = false;
       const PieceKeys<NR, TK> keys(a, w);
       const PageAhead<NR, TK> pages(a, w, keys);
       // lane i < per: the tile's page i
@@ -354,6 +356,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
       }
     }
     static_assert(kMaxPages <= 32, "a lane per page");
+    if (lane == 0 && first) w.write_meta(true);
     if (*abort) {  // the copies in flight land before the CTA can end
       for (int i = n > NS ? n - NS : 0; i < n; ++i) mbar_wait(&full[i % NS], (uint32_t)(i / NS) & 1u, a.status, kDrainLimitNs);
     }
@@ -423,10 +426,8 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
     const bool has_dim = D == 128 || lane < 16;
     const int dim = D == 128 ? tid : warp * 16 + (lane & 15);  // M = 64 accumulators lie in lanes 0-15
-    bool ok = true, first = true;
+    bool ok = true;
     while (ok && w.next()) {
-      if (tid == 0 && first) w.write_meta(false);
-      first = false;
       const PieceKeys<NR, TK> keys(a, w);
       const int rows = w.rows(), r0 = w.p_mt * NR;
       const bool work = keys.t0 < w.p_t1;
@@ -642,7 +643,6 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
         }
       }
     }
-    if (first && tid == 0) w.write_meta(true);
   }
   tc_fence_before();
   __syncthreads();
@@ -756,6 +756,20 @@ __device__ __forceinline__ float many_top(const PagedLaunch& a, const ManyRow& r
 }
 
 template <int D>
+__device__ __forceinline__ void many_rescale(uint32_t o_addr, float alpha) {
+#pragma unroll 1
+  for (int d = 0; d < D; d += 32) {
+    uint32_t o[32];
+    tmem_ld(o_addr + d, o);
+    tmem_ld_done(o);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+    tmem_st_32(o_addr + d, o);
+  }
+  tmem_st_wait();
+}
+
+template <int D>
 __global__ void __launch_bounds__(kManyThreads, 1)
     paged_many_kernel(const __grid_constant__ PagedLaunch a, const __grid_constant__ CUtensorMap map_k, const WaitTest test) {
   using C = ManyCfg<D>;
@@ -810,8 +824,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const int per = TK >> a.page_log2;
     const uint32_t page_bytes = (uint32_t)a.page * D;
     int n = 0;
-    bool go = true;
+    bool go = true, first = true;
     while (go && w.next()) {
+      if (lane == 0 && first) w.write_meta(false);
+      first = false;
       const PieceKeys<M, TK> keys(a, w);
       const PageAhead<M, TK> pages(a, w, keys);
       // lane i < per: the tile's page i
@@ -836,6 +852,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         __syncwarp();
       }
     }
+    if (lane == 0 && first) w.write_meta(true);
     if (*abort)
       for (int i = n > 2 ? n - 2 : 0; i < n; ++i) mbar_wait(&k_full[i & 1], (uint32_t)(i >> 1) & 1u, a.status, kDrainLimitNs);
     __syncwarp();
@@ -939,64 +956,60 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       named_sync(2, 128);
       const float vref = __int_as_float(*vref_s);
       if (lane == 0) mbar_arrive(ref_full);
-      const float inv = vref > 0.f ? __fdividef(1.f, vref) * 32768.f : 0.f;
-      uint4 raw[IT];
-      float sc[2];  // scales of the warp's keys 0-15 and 16-31 (0: not there)
-      int32_t e[2];  // pages of the same keys of the tile to fetch next
+      // codes to f16 (exact) and times 2^7 scale / vref: at most 448 * 2^7
+      const float inv = vref > 0.f ? __fdividef(1.f, vref) * 128.f : 0.f;
+      // A warp's 32 keys in two halves of 16 (one page each): a half's codes
+      // are asked for two halves ahead of their conversion.
+      constexpr int HI = IT / 2;
+      uint4 raw[2][HI];
+      float sc[2];  // the halves' scales (0: not there)
+      int32_t e[2];
       auto entries = [&](int t) {
         e[0] = pages.entry(t, t * TK + v * 32);
         e[1] = pages.entry(t, t * TK + v * 32 + 16);
       };
-      auto fetch = [&](int t) {
-        const int j0 = t * TK + v * 32;
-        const int64_t p0 = pages.place(e[0]), p1 = pages.place(e[1]);
-        sc[0] = ld_if(a.v_scale + p0, p0 >= 0, 0.f);
-        sc[1] = ld_if(a.v_scale + p1, p1 >= 0, 0.f);
+      auto fetch = [&](int t, int half) {
+        const int64_t ph = pages.place(e[half]);
+        sc[half] = ld_if(a.v_scale + ph, ph >= 0, 0.f);
+        const int j0 = t * TK + v * 32 + half * 16 + rsub;
+        const uint8_t* src = a.v + (ph * a.page + (j0 & (a.page - 1))) * D + c * 16;
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-          const int r = i * RPI + rsub, j = j0 + r;
-          const int64_t ph = i < IT / 2 ? p0 : p1;
-          raw[i] = ld_if(a.v + (ph * a.page + (j & (a.page - 1))) * D + c * 16, ph >= 0 && j < keys.hi);
-        }
+        for (int i = 0; i < HI; ++i)
+          raw[half][i] = ld_if(src + i * RPI * D, ph >= 0 && j0 + i * RPI < keys.hi);
       };
       entries(keys.t0);
-      fetch(keys.t0);
+      fetch(keys.t0, 0);
+      fetch(keys.t0, 1);
       entries(keys.t0 + 1);
       for (int t = keys.t0; t < keys.t1; ++t, ++n) {
         const int b = n & 1;
         if (n >= 2 && !(ok = wait(&v_empty[b], (uint32_t)((n >> 1) - 1) & 1u))) break;
-        const uint32_t dst = smem_u32(sm + C::OFF_V + b * C::kV);
-        // codes to f16 (exact), times 2^15 scale / vref / 2^8: the code's bits
-        // as an f16 read 2^-8 of its value, so the factor is 2^15 at most
-        const __half2 f[2] = {__float2half2_rn(sc[0] * inv), __float2half2_rn(sc[1] * inv)};
+        const uint32_t dst = smem_u32(sm + C::OFF_V + b * C::kV) + (c / 4) * (TK * 128);  // the 64-dim atom
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-          const uint32_t wd[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-          uint32_t h[8];
+        for (int half = 0; half < 2; ++half) {
+          const __half2 f = __float2half2_rn(sc[half] * inv);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            // bytes to the high halves of 16-bit lanes, then the exponent and mantissa one bit down
-            const uint32_t u0 = __byte_perm(wd[q], 0, 0x1404), u1 = __byte_perm(wd[q], 0, 0x3424);
-            const uint32_t e0 = (u0 & 0x80008000u) | ((u0 & 0x7f007f00u) >> 1);
-            const uint32_t e1 = (u1 & 0x80008000u) | ((u1 & 0x7f007f00u) >> 1);
-            const __half2 m0 = __hmul2(*reinterpret_cast<const __half2*>(&e0), f[i >= IT / 2]);
-            const __half2 m1 = __hmul2(*reinterpret_cast<const __half2*>(&e1), f[i >= IT / 2]);
-            h[2 * q] = *reinterpret_cast<const uint32_t*>(&m0);
-            h[2 * q + 1] = *reinterpret_cast<const uint32_t*>(&m1);
+          for (int i = 0; i < HI; ++i) {
+            const uint32_t wd[4] = {raw[half][i].x, raw[half][i].y, raw[half][i].z, raw[half][i].w};
+            uint32_t h[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const __half2 x(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(wd[q / 2] >> (16 * (q & 1))), __NV_E4M3));
+              const __half2 y = __hmul2(x, f);
+              h[q] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            // 16 dims are two chunks of the atom; the lanes of the second atom
+            // store theirs in the other order, so that a store covers all banks
+            const int r = v * 32 + half * 16 + i * RPI + rsub, ch = (c % 4) * 2, flip = (c / 4) & 1;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const bool second = (q ^ flip) != 0;
+              st_shared16(dst + swz<128>(r, (ch + (q ^ flip)) * 16), second ? h[4] : h[0], second ? h[5] : h[1],
+                          second ? h[6] : h[2], second ? h[7] : h[3]);
+            }
           }
-          // 16 dims are two chunks of a 64-dim atom; the lanes of the second
-          // atom store theirs in the other order, so that a store covers all banks
-          const int r = v * 32 + i * RPI + rsub, atom = c / 4, ch = (c % 4) * 2;
-          const bool flip = (c / 4) & 1;
-          const uint32_t at = dst + atom * (TK * 128);
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const bool second = (q == 1) != flip;
-            st_shared16(at + swz<128>(r, (ch + (second ? 1 : 0)) * 16), second ? h[4] : h[0], second ? h[5] : h[1],
-                        second ? h[6] : h[2], second ? h[7] : h[3]);
-          }
+          fetch(t + 1, half);
         }
-        fetch(t + 1);
         entries(t + 2);
         fence_async_smem();
         __syncwarp();
@@ -1011,11 +1024,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const float cap2 = a.cap * kPagedLog2e;
     const uint32_t lane_base = (uint32_t)((warp % 4) * 32) << 16;
     const uint32_t s_addr = tmem + g * 128 + lane_base, o_addr = tmem + 256 + g * 128 + lane_base;
-    bool ok = true, first = true;
+    bool ok = true;
     int cnt = 0, pieces = 0, merges = 0;
     while (ok && w.next()) {
-      if (tid == 0 && first) w.write_meta(false);
-      first = false;
       const PieceKeys<M, TK> keys(a, w);
       const int rows = w.rows();
       // Up to 128 rows are one tile that both warpgroups work on, taking its
@@ -1126,16 +1137,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           if (!fresh && !(ok = wait(&pv_done[g], (uint32_t)(cnt - 1) & 1u))) break;
           if (__any_sync(0xffffffffu, grown)) {
             tc_fence_after();
-#pragma unroll 1
-            for (int d = 0; d < D; d += 32) {
-              uint32_t o[32];
-              tmem_ld(o_addr + d, o);
-              tmem_ld_done(o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st_32(o_addr + d, o);
-            }
-            tmem_st_wait();
+            many_rescale<D>(o_addr, alpha);
           }
           const float ref = m_ref == -INFINITY ? 0.f : m_ref;
           const uint64_t ref2 = pack2(-ref, -ref);
@@ -1261,7 +1263,6 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(piece_done);
     }
-    if (first && tid == 0) w.write_meta(true);
   }
   tc_fence_before();
   __syncthreads();
