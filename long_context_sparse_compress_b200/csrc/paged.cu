@@ -648,36 +648,62 @@ __global__ void __launch_bounds__(kFmaThreads) paged_fma_kernel(const __grid_con
 
 // ---------------------------------------------------------- split items
 // Joins the pieces of an item in CTA order: O = sum_i 2^(m_i - m) O_i and the
-// same for the sums.  The CTA of the item's second piece does it; D threads, a
-// dim each, up to 32 CTAs per item sharing its rows.
-constexpr int kCombineY = 32;
+// same for the sums.  The CTAs of the item's second piece do it, a warp for a
+// row: a lane per piece for the maxima and sums, then 4 (D = 64: 2) dims per
+// lane over the pieces.
+constexpr int kCombineRows = 8;
 
 template <int D>
-__global__ void __launch_bounds__(D) paged_combine_kernel(PagedLaunch a, int M) {
+__global__ void __launch_bounds__(kCombineRows * 32) paged_combine_kernel(PagedLaunch a, int M) {
   grid_dep_wait();
-  const int c = blockIdx.x, d = threadIdx.x;
+  constexpr int VPL = D / 32;
+  const int c = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * kCombineRows + threadIdx.x / 32;
   const int32_t* m = a.meta + 8 * (int64_t)c;
-  const int b = m[0], c0 = m[3], c1 = m[4];
+  const int b = m[0], h = m[1], mt = m[2], c0 = m[3], c1 = m[4];
   if (b < 0 || c != c0 + 1) return;
-  const int h = m[1], mt = m[2];
   const PagedSeq s = paged_seq(a, b);
-  const int rows = min(M, s.n * a.G - mt * M);
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    float top = -INFINITY;
-    for (int i = c0; i <= c1; ++i) {
-      const int64_t at = (2 * (int64_t)i + (i == c0 ? 1 : 0)) * M + r;
-      top = fmaxf(top, a.part_ml[at * 2]);
-    }
-    const float ref = top == -INFINITY ? 0.f : top;
-    float o = 0.f, l = 0.f;
+  if (r >= min(M, s.n * a.G - mt * M)) return;
+  // the place of piece i's row
+  auto place = [&](int i) { return (2 * (int64_t)i + (i == c0 ? 1 : 0)) * M + r; };
+  float top = -INFINITY, l = 0.f, o[VPL] = {};
+  for (int i0 = c0; i0 <= c1; i0 += 32) {  // 32 pieces at a time
+    const int n = min(32, c1 - i0 + 1);
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < n) ml = *reinterpret_cast<const float2*>(a.part_ml + place(i0 + lane) * 2);
+    const float high = fmaxf(top, warp_max(ml.x)), ref = high == -INFINITY ? 0.f : high;
+    const float old = paged_ex2(top - ref), f = paged_ex2(ml.x - ref);
+    top = high;
+    l = fmaf(l, old, warp_sum(ml.y * f));
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) o[k] *= old;
 #pragma unroll 4
-    for (int i = c0; i <= c1; ++i) {
-      const int64_t at = (2 * (int64_t)i + (i == c0 ? 1 : 0)) * M + r;
-      const float f = paged_ex2(a.part_ml[at * 2] - ref);
-      l = fmaf(f, a.part_ml[at * 2 + 1], l);
-      o = fmaf(f, a.part_o[at * D + d], o);
+    for (int i = 0; i < n; ++i) {
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+      const float* p = a.part_o + place(i0 + i) * D + lane * VPL;
+      float v[VPL];
+      if constexpr (VPL == 4) {
+        const float4 u = *reinterpret_cast<const float4*>(p);
+        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+      } else {
+        const float2 u = *reinterpret_cast<const float2*>(p);
+        v[0] = u.x, v[1] = u.y;
+      }
+#pragma unroll
+      for (int k = 0; k < VPL; ++k) o[k] = fmaf(fi, v[k], o[k]);
     }
-    paged_write<D>(a, s, h, mt * M + r, d, o, top, l);
+  }
+  int64_t at;
+  const float f = paged_close(a, s, h, mt * M + r, top, l, lane == 0, &at);
+#pragma unroll
+  for (int k = 0; k < VPL; ++k) o[k] = f == 0.f ? 0.f : o[k] * f;
+  at = at * D + lane * VPL;
+#pragma unroll
+  for (int k = 0; k < VPL; k += 2) {
+    if (a.q_dtype == LCSC_DT_BF16)
+      *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out) + at + k) =
+          (uint32_t)bf16_code(o[k]) | ((uint32_t)bf16_code(o[k + 1]) << 16);
+    else
+      *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + at + k) = make_float2(o[k], o[k + 1]);
   }
 }
 
@@ -729,9 +755,9 @@ cudaError_t launch_paged_attn(const PagedLaunch& a, const PagedForm& f, cudaStre
   cudaError_t e = f.kind ? launch_paged_mma(a, f, stream)
                   : a.D == 128 ? launch_fma<128>(a, stream) : launch_fma<64>(a, stream);
   if (e != cudaSuccess || a.ctas == 1) return e;
-  const dim3 grid(a.ctas, f.rows < kCombineY ? f.rows : kCombineY);
-  return a.D == 128 ? launch_pdl(paged_combine_kernel<128>, grid, dim3(128), 0, stream, a, f.rows)
-                    : launch_pdl(paged_combine_kernel<64>, grid, dim3(64), 0, stream, a, f.rows);
+  const dim3 grid(a.ctas, f.rows / kCombineRows), block(kCombineRows * 32);
+  return a.D == 128 ? launch_pdl(paged_combine_kernel<128>, grid, block, 0, stream, a, f.rows)
+                    : launch_pdl(paged_combine_kernel<64>, grid, block, 0, stream, a, f.rows);
 }
 
 }  // namespace lcsc

@@ -412,26 +412,33 @@ __device__ __forceinline__ float paged_cap(float x, float cap) {
   return cap - __fdividef(2.f * cap, e + 1.f);
 }
 
-// One output value (row = token * G + head in group, dim d) from the sum O of
-// the weights' products, their max (base-2 units) and sum; d = 0 writes lse.
-template <int D>
-__device__ __forceinline__ void paged_write(const PagedLaunch& a, const PagedSeq& s, int h, int row, int d, float o,
-                                            float top, float l) {
+// What a finished row's sum O of the weights' products is multiplied by, from
+// their max (base-2 units) and sum; the row's place in out and lse, which is
+// written by the one thread that says so.  row = token * G + head in group.
+__device__ __forceinline__ float paged_close(const PagedLaunch& a, const PagedSeq& s, int h, int row, float top,
+                                             float l, bool write_lse, int64_t* at) {
   const int i = paged_div(a, row), head = h * a.G + row - i * a.G;
-  const int64_t at = (s.q0 + i) * a.Hq + head;
+  *at = (s.q0 + i) * a.Hq + head;
+  float f = 1.f;
   if (a.sink && s.L > 0) {
     const float sg = a.sink[head] * kPagedLog2e, m = fmaxf(top, sg);
-    const float f = paged_ex2(top - m);  // top -inf: 0
     if (m != -INFINITY) {
-      o *= f;
+      f = paged_ex2(top - m);  // top -inf: 0
       l = fmaf(l, f, paged_ex2(sg - m));
       top = m;
     }
   }
-  const float r = l > 0.f ? o / l : 0.f;
+  if (write_lse && a.lse) a.lse[*at] = l == 0.f ? -INFINITY : (top + log2f(l)) * kPagedLn2;
+  return l == 0.f ? 0.f : f / l;  // a sum that is no number stays one
+}
+
+template <int D>
+__device__ __forceinline__ void paged_write(const PagedLaunch& a, const PagedSeq& s, int h, int row, int d, float o,
+                                            float top, float l) {
+  int64_t at;
+  const float f = paged_close(a, s, h, row, top, l, d == 0, &at), r = f == 0.f ? 0.f : o * f;
   if (a.q_dtype == LCSC_DT_BF16) reinterpret_cast<uint16_t*>(a.out)[at * D + d] = bf16_code(r);
   else reinterpret_cast<float*>(a.out)[at * D + d] = r;
-  if (a.lse && d == 0) a.lse[at] = l > 0.f ? (top + log2f(l)) * kPagedLn2 : -INFINITY;
 }
 
 #endif

@@ -813,7 +813,9 @@ __device__ __forceinline__ void many_rescale(uint32_t o_addr, float alpha) {
   tmem_st_wait();
 }
 
-template <int D>
+// GEN: scores are capped or biased (both forms of the loop in one kernel cost the
+// plain one GENCOST).
+template <int D, bool GEN>
 __global__ void __launch_bounds__(kManyThreads, 1)
     paged_many_kernel(const __grid_constant__ PagedLaunch a, const __grid_constant__ CUtensorMap map_k, const WaitTest test) {
   using C = ManyCfg<D>;
@@ -1002,62 +1004,64 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       if (lane == 0) mbar_arrive(ref_full);
       // codes to f16 (exact) and times 2^7 scale / vref: at most 448 * 2^7
       const float inv = vref > 0.f ? __fdividef(1.f, vref) * 128.f : 0.f;
-      // A warp's 32 keys in two halves of 16 (one page each): a half's codes
-      // are asked for two halves ahead of their conversion.
+      // A warp's 32 keys of a tile in two halves of 16 (one page each), a rolled
+      // loop over the halves: while one is converted and stored the next one's
+      // page is looked up, and its codes are asked for as soon as the registers
+      // are free.
       constexpr int HI = IT / 2;
-      uint4 raw[2][HI];
-      float sc[2];  // the halves' scales (0: not there)
-      int32_t e[2];
-      auto entries = [&](int t) {
-        e[0] = pages.entry(t, t * TK + v * 32);
-        e[1] = pages.entry(t, t * TK + v * 32 + 16);
-      };
-      auto fetch = [&](int t, int half) {
-        const int64_t ph = pages.place(e[half]);
-        sc[half] = ld_if(a.v_scale + ph, ph >= 0, 0.f);
-        const int j0 = t * TK + v * 32 + half * 16 + rsub;
+      uint4 raw[HI];
+      float sc;  // the half's scale (0: not there)
+      int j = keys.t0 * TK + v * 32;  // the half's first key
+      auto entry = [&](int key) { return pages.entry(key / TK, key); };
+      auto fetch = [&](int32_t e, int key) {
+        const int64_t ph = pages.place(e);
+        sc = ld_if(a.v_scale + ph, ph >= 0, 0.f);
+        const int j0 = key + rsub;
         const uint8_t* src = a.v + (ph * a.page + (j0 & (a.page - 1))) * D + c * 16;
 #pragma unroll
-        for (int i = 0; i < HI; ++i)
-          raw[half][i] = ld_if(src + i * RPI * D, ph >= 0 && j0 + i * RPI < keys.hi);
+        for (int i = 0; i < HI; ++i) raw[i] = ld_if(src + i * RPI * D, ph >= 0 && j0 + i * RPI < keys.hi);
       };
-      entries(keys.t0);
-      fetch(keys.t0, 0);
-      fetch(keys.t0, 1);
-      entries(keys.t0 + 1);
-      for (int t = keys.t0; t < keys.t1; ++t, ++n) {
-        const int b = n & 1;
-        if (n >= 2 && !(ok = wait(&v_empty[b], (uint32_t)((n >> 1) - 1) & 1u))) break;
-        const uint32_t dst = smem_u32(sm + C::OFF_V + b * C::kV) + (c / 4) * (TK * 128);  // the 64-dim atom
+      fetch(entry(j), j);
+      int32_t e1 = entry(j + 16);
+      const int flip = (c / 4) & 1;
+      const uint32_t to = smem_u32(sm + C::OFF_V) + (c / 4) * (TK * 128);  // the 64-dim atom
+#pragma unroll 1
+      for (int u = 2 * keys.t0; u < 2 * keys.t1; ++u) {
+        const int half = u & 1, b = n & 1;
+        const int jn = half ? j - 16 + TK : j + 16;  // the next half, and the one after it
+        const int32_t e2 = entry(half ? jn + 16 : jn - 16 + TK);
+        if (half == 0 && n >= 2 && !(ok = wait(&v_empty[b], (uint32_t)((n >> 1) - 1) & 1u))) break;
+        const __half2 f = __float2half2_rn(sc * inv);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const __half2 f = __float2half2_rn(sc[half] * inv);
+        for (int i = 0; i < HI; ++i) {
+          const uint32_t wd[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+          uint32_t h[8];
 #pragma unroll
-          for (int i = 0; i < HI; ++i) {
-            const uint32_t wd[4] = {raw[half][i].x, raw[half][i].y, raw[half][i].z, raw[half][i].w};
-            uint32_t h[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const __half2 x(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(wd[q / 2] >> (16 * (q & 1))), __NV_E4M3));
-              const __half2 y = __hmul2(x, f);
-              h[q] = *reinterpret_cast<const uint32_t*>(&y);
-            }
-            // 16 dims are two chunks of the atom; the lanes of the second atom
-            // store theirs in the other order, so that a store covers all banks
-            const int r = v * 32 + half * 16 + i * RPI + rsub, ch = (c % 4) * 2, flip = (c / 4) & 1;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const bool second = (q ^ flip) != 0;
-              st_shared16(dst + swz<128>(r, (ch + (q ^ flip)) * 16), second ? h[4] : h[0], second ? h[5] : h[1],
-                          second ? h[6] : h[2], second ? h[7] : h[3]);
-            }
+          for (int q = 0; q < 8; ++q) {
+            const __half2 x(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(wd[q / 2] >> (16 * (q & 1))), __NV_E4M3));
+            const __half2 y = __hmul2(x, f);
+            h[q] = *reinterpret_cast<const uint32_t*>(&y);
           }
-          fetch(t + 1, half);
+          // 16 dims are two chunks of the atom; the lanes of the second atom
+          // store theirs in the other order, so that a store covers all banks
+          const int r = v * 32 + half * 16 + i * RPI + rsub, ch = (c % 4) * 2;
+          const uint32_t at = to + b * C::kV;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const bool second = (q ^ flip) != 0;
+            st_shared16(at + swz<128>(r, (ch + (q ^ flip)) * 16), second ? h[4] : h[0], second ? h[5] : h[1],
+                        second ? h[6] : h[2], second ? h[7] : h[3]);
+          }
         }
-        entries(t + 2);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&v_full[b]);
+        fetch(e1, jn);
+        e1 = e2;
+        j = jn;
+        if (half == 1) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&v_full[b]);
+          ++n;
+        }
       }
       if (!(ok = named_and(2, 128, ok))) break;  // the four warps go on or stop together
     }
@@ -1164,10 +1168,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           const bool inside = __all_sync(0xffffffffu, r.lo <= j0 && r.hi >= j0 + TK && (lane / 8 != of4 || ks >= 0.f));
           if (!(ok = wait(&s_full[g], (uint32_t)cnt & 1u))) break;
           tc_fence_after();
-          const ManyForm form = a.cap > 0.f || a.slopes ? kScores : inside ? kPlain : kMasked;
-          const float top = form == kPlain    ? many_top<kPlain>(a, r, cap2, ks, 8 * of4, j0, s_addr)
-                            : form == kMasked ? many_top<kMasked>(a, r, cap2, ks, 8 * of4, j0, s_addr)
-                                              : many_top<kScores>(a, r, cap2, ks, 8 * of4, j0, s_addr);
+          const bool plain = !GEN && inside;  // the products are the scores but for a factor
+          float top;
+          if constexpr (GEN) top = many_top<kScores>(a, r, cap2, ks, 8 * of4, j0, s_addr);
+          else if (plain) top = many_top<kPlain>(a, r, cap2, ks, 8 * of4, j0, s_addr);
+          else top = many_top<kMasked>(a, r, cap2, ks, 8 * of4, j0, s_addr);
           const bool fresh = t == t_first;
           float alpha = 1.f;
           bool grown = false;
@@ -1192,7 +1197,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             tmem_ld(s_addr + h, x);
             const float k0 = __shfl_sync(0xffffffffu, ks, 8 * of4 + (h >> 4)),
                         k1 = __shfl_sync(0xffffffffu, ks, 8 * of4 + (h >> 4) + 1);
-            const float c0 = form == kPlain ? k0 * r.rf : 1.f, c1 = form == kPlain ? k1 * r.rf : 1.f;
+            const float c0 = plain ? k0 * r.rf : 1.f, c1 = plain ? k1 * r.rf : 1.f;
             const uint64_t c02 = pack2(c0, c0), c12 = pack2(c1, c1);
             tmem_ld_done(x);
 #pragma unroll
@@ -1245,24 +1250,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       // O (times 2^7 / vref), the row's maximum and sum
       if (!(shared && g == 1)) {
         const float unit = vref * (1.f / 128.f);
-        const int row = r0 + row_in;
-        const int tok = paged_div(a, row), head = w.p_h * a.G + row - tok * a.G;
-        const int64_t at = (w.p_s.q0 + tok) * a.Hq + head;
+        int64_t at = 0;
         const int64_t part = w.slot() * M + r_in;
         float f = unit;
-        if (w.whole()) {
-          float top = m_ref, den = l;
-          if (mine && a.sink && w.p_s.L > 0) {
-            const float sg = a.sink[head] * kPagedLog2e, m = fmaxf(top, sg);
-            if (m != -INFINITY) {
-              const float e = paged_ex2(top - m);
-              f *= e;
-              den = fmaf(den, e, paged_ex2(sg - m));
-              top = m;
-            }
-          }
-          f = den > 0.f ? f / den : den == 0.f ? 0.f : den;  // a sum that is no number stays one
-          if (mine && a.lse) a.lse[at] = den == 0.f ? -INFINITY : (top + log2f(den)) * kPagedLn2;
+        if (mine && w.whole()) {
+          f *= paged_close(a, w.p_s, w.p_h, r0 + row_in, m_ref, l, true, &at);
         } else if (mine) {
           a.part_ml[part * 2] = m_ref;
           a.part_ml[part * 2 + 1] = l;
@@ -1353,7 +1345,7 @@ cudaError_t launch_few(const PagedLaunch& a, const CUtensorMap& k, const CUtenso
 
 template <int D>
 cudaError_t launch_many(const PagedLaunch& a, const CUtensorMap& k, cudaStream_t stream) {
-  auto kern = paged_many_kernel<D>;
+  auto kern = a.cap > 0.f || a.slopes ? paged_many_kernel<D, true> : paged_many_kernel<D, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ManyCfg<D>::SMEM);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(a.ctas), dim3(kManyThreads), ManyCfg<D>::SMEM, stream, a, k, wait_test());
