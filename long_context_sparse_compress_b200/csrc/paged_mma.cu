@@ -764,7 +764,7 @@ __device__ __forceinline__ void many_bias(float (&v)[32], const ManyRow& r, int 
 enum ManyForm { kPlain, kMasked, kScores };
 template <ManyForm F>
 __device__ __forceinline__ float many_top(const PagedLaunch& a, const ManyRow& r, float cap2, float ks, int of, int j0,
-                                          uint32_t s_addr) {
+                                          bool inside, uint32_t s_addr) {
   float top = -INFINITY;
 #pragma unroll 1
   for (int h = 0; h < 128; h += 32) {
@@ -784,7 +784,11 @@ __device__ __forceinline__ float many_top(const PagedLaunch& a, const ManyRow& r
         if (a.slopes) many_bias(v, r, j0 + h);
       }
 #pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = seen >> i & 1u ? __float_as_uint(v[i]) : 0xff800000u;
+      for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(v[i]);
+      if (!inside) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = seen >> i & 1u ? x[i] : 0xff800000u;
+      }
       tmem_st_32(s_addr + h, x);
     }
     float m0 = __uint_as_float(x[0]), m1 = __uint_as_float(x[16]);
@@ -1170,9 +1174,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           tc_fence_after();
           const bool plain = !GEN && inside;  // the products are the scores but for a factor
           float top;
-          if constexpr (GEN) top = many_top<kScores>(a, r, cap2, ks, 8 * of4, j0, s_addr);
-          else if (plain) top = many_top<kPlain>(a, r, cap2, ks, 8 * of4, j0, s_addr);
-          else top = many_top<kMasked>(a, r, cap2, ks, 8 * of4, j0, s_addr);
+          if constexpr (GEN) top = many_top<kScores>(a, r, cap2, ks, 8 * of4, j0, inside, s_addr);
+          else if (plain) top = many_top<kPlain>(a, r, cap2, ks, 8 * of4, j0, inside, s_addr);
+          else top = many_top<kMasked>(a, r, cap2, ks, 8 * of4, j0, inside, s_addr);
           const bool fresh = t == t_first;
           float alpha = 1.f;
           bool grown = false;
