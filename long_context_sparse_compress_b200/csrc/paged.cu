@@ -249,15 +249,6 @@ __device__ __forceinline__ bool store_load(const void* x, int64_t at, int dtype,
   return bad;
 }
 
-// |v|, or 0 for what is not finite.
-constexpr float kMostFinite = 3.402823466e38f;
-__device__ __forceinline__ float finite(float v, bool& bad) {
-  const float m = fabsf(v);
-  if (m <= kMostFinite) return m;
-  bad = true;
-  return 0.f;
-}
-
 template <int VPL>
 __device__ __forceinline__ float store_amax(const float (&v)[VPL]) {
   float a = 0.f;
@@ -299,6 +290,32 @@ __device__ __forceinline__ void chunk_values(const uint4& u, float (&v)[F32 ? 4 
       v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
+}
+
+// Its largest magnitude, as float32 bits.
+template <bool F32>
+__device__ __forceinline__ uint32_t chunk_amax(const uint4& u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = F32 ? max(m, w[i] & 0x7fffffffu) : __vmaxu2(m, w[i] & 0x7fff7fffu);
+  return F32 ? m : max(m << 16, m & 0xffff0000u);
+}
+
+// Zero in the place of the values that are not finite.
+template <bool F32>
+__device__ __forceinline__ void chunk_finite(uint4& u) {
+  uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (F32) {
+      if ((w[i] & 0x7fffffffu) >= 0x7f800000u) w[i] = 0;
+    } else {
+      if ((w[i] & 0x7fffu) >= 0x7f80u) w[i] &= 0xffff0000u;
+      if ((w[i] & 0x7fff0000u) >= 0x7f800000u) w[i] &= 0xffffu;
+    }
+  }
+  u = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <int VPL, int TILE, bool F32, int IT>
@@ -402,7 +419,7 @@ __global__ void __launch_bounds__(kStoreWarps * 32) paged_store_kernel(PagedStor
         const float old = first > 0 ? scales[ph] : 0.f;
         const uint8_t* src = reinterpret_cast<const uint8_t*>(x) + ((t0 + i) * stride + h * D) * (F32 ? 4 : 2);
         uint4 u[IT];
-        float amax = 0.f;
+        uint32_t amax = 0;  // float32 bits of the largest magnitude, which order as the numbers do
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
           const int c = tid + k * kStoreWarps * 32, row = c / CPR;
@@ -410,15 +427,19 @@ __global__ void __launch_bounds__(kStoreWarps * 32) paged_store_kernel(PagedStor
           if (row < n) u[k] = *reinterpret_cast<const uint4*>(src + row * stride * (F32 ? 4 : 2) + (c % CPR) * 16);
         }
 #pragma unroll
-        for (int k = 0; k < IT; ++k) {
-          float v[VPC];
-          chunk_values<F32>(u[k], v);
+        for (int k = 0; k < IT; ++k) amax = max(amax, chunk_amax<F32>(u[k]));
+        // some value is not finite; with the barrier before this run's maxima
+        if (__syncthreads_or(amax >= 0x7f800000u)) {
+          bad |= amax >= 0x7f800000u;
+          amax = 0;
 #pragma unroll
-          for (int q = 0; q < VPC; ++q) amax = fmaxf(amax, finite(v[q], bad));
+          for (int k = 0; k < IT; ++k) {
+            chunk_finite<F32>(u[k]);
+            amax = max(amax, chunk_amax<F32>(u[k]));
+          }
         }
-        amax = warp_max(amax);
-        __syncthreads();  // the last run's maxima are read, the old scale too
-        if (lane == 0) red[warp] = __float_as_int(amax);
+        amax = __reduce_max_sync(0xffffffffu, amax);
+        if (lane == 0) red[warp] = (int)amax;
         __syncthreads();
         int top = red[0];
 #pragma unroll
@@ -435,12 +456,9 @@ __global__ void __launch_bounds__(kStoreWarps * 32) paged_store_kernel(PagedStor
           chunk_values<F32>(u[k], v);
           uint32_t code[VPC / 4];
 #pragma unroll
-          for (int q = 0; q < VPC / 4; ++q) {
-            float y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = fabsf(v[4 * q + e]) <= kMostFinite ? v[4 * q + e] * inv : 0.f;
-            code[q] = e4m3x2_code(y[0], y[1]) | ((uint32_t)e4m3x2_code(y[2], y[3]) << 16);
-          }
+          for (int q = 0; q < VPC / 4; ++q)
+            code[q] = e4m3x2_code(v[4 * q] * inv, v[4 * q + 1] * inv) |
+                      ((uint32_t)e4m3x2_code(v[4 * q + 2] * inv, v[4 * q + 3] * inv) << 16);
           uint8_t* dst = page + (int64_t)(first + row) * D + (c % CPR) * VPC;
           if constexpr (F32) *reinterpret_cast<uint32_t*>(dst) = code[0];
           else *reinterpret_cast<uint2*>(dst) = make_uint2(code[0], code[VPC / 4 - 1]);

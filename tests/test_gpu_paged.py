@@ -145,6 +145,25 @@ def test_store_extremes(cuda_lib):
     assert torch.equal(cache.k, cache.v)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("P,n", [(128, 100), (64, 64), (16, 16), (32, 5)])
+def test_store_of_values_that_are_not_finite(cuda_lib, dtype, P, n):
+    """They are stored as zeros, left out of the scale and reported, in runs of every length."""
+    rng = np.random.default_rng(P)
+    x = torch.from_numpy(rng.standard_normal((n, 2, 128)).astype(np.float32)).to(dtype)
+    for i, v in enumerate((float("nan"), float("inf"), -float("inf"), -float("nan"))):
+        x[i, 0, 5 + 31 * i] = v
+    cache = L.PagedCache(2, 2, P, 128)
+    p, st = L.paged_params(2, 2, 128, P, x_dtype="f32" if dtype == F32 else "bf16"), status0()
+    clean = torch.nan_to_num(x.float(), 0, 0, 0).to(dtype)
+    L.paged_store(p, cache, x.cuda(), clean.cuda(), i32(np.arange(n)), status=st)
+    assert st.item() == L.DEV_RANGE
+    assert torch.equal(cache.k, cache.v) and torch.equal(cache.k_scale, cache.v_scale)
+    codes, scale = np.zeros((2, 2, P, 128), np.uint8), np.ones((2, 2), np.float32)
+    paged.store(codes, scale, x.float().numpy(), np.arange(n), P)
+    assert np.array_equal(cache.k.cpu().numpy(), codes) and np.array_equal(cache.k_scale.cpu().numpy(), scale)
+
+
 # --------------------------------------------------------------- attention
 
 class Case:
