@@ -470,7 +470,7 @@ typedef struct lcsc_paged_params {
   int32_t x_dtype;     /* LCSC_DT_*: K and V rows given to the store */
   float sm_scale;      /* softmax scale of q.K (> 0) */
   int32_t window;      /* > 0: a query sees the last `window` tokens only, its own included; 0: all */
-  float softcap;       /* c > 0: scores are capped to c tanh(score / c); 0: off */
+  float softcap;       /* c in [1e-6, 1e4]: scores are capped to c tanh(score / c); 0: off */
 } lcsc_paged_params;
 
 typedef struct lcsc_paged_cache {
@@ -545,6 +545,10 @@ int32_t lcsc_paged_store(const lcsc_paged_params* p, const lcsc_paged_cache* cac
  * pool hides its tokens (LCSC_DEV_BAD_INDEX); pages that no query of the step
  * sees are not looked at.  Codes of visible tokens are never 0x7F or 0xFF (the
  * store writes none); rows of a page past the request's end may hold anything.
+ * The workspace (lcsc_paged_attn_workspace_size() bytes, the same for every
+ * length) serves one call at a time: calls that may overlap, replays of
+ * captured ones among them, need one each.  Results do not depend on what ran
+ * before or beside: every sum has a fixed order.
  * BF16 queries run on the tensor cores with float32 sums: the query is the sum
  * of E4M3 terms (values below 2^-10 of a head's largest keep an absolute
  * precision of 2^-17 of it), the softmax weights are held to 11 bits or more;

@@ -226,7 +226,8 @@ int32_t check_paged(const lcsc_paged_params* p) {
   if (p->n_heads < 1 || p->n_kv_heads < 1 || p->n_heads % p->n_kv_heads) return LCSC_ERR_INVALID_ARG;
   if (!valid_dt(p->q_dtype) || !valid_dt(p->x_dtype)) return LCSC_ERR_INVALID_ARG;
   if (!(p->sm_scale > 0.f) || p->sm_scale == INFINITY || p->window < 0) return LCSC_ERR_INVALID_ARG;
-  if (!(p->softcap >= 0.f) || p->softcap == INFINITY) return LCSC_ERR_INVALID_ARG;
+  // (below, no score is told from another; above, 1e-7 of the cap is more than a weight's rounding)
+  if (!(p->softcap == 0.f || (p->softcap >= 1e-6f && p->softcap <= 1e4f))) return LCSC_ERR_INVALID_ARG;
   if (!valid_page(p->page_size) || (p->head_dim != 64 && p->head_dim != 128)) return LCSC_ERR_UNSUPPORTED;
   if (p->n_heads > 65535) return LCSC_ERR_UNSUPPORTED;
   return LCSC_OK;

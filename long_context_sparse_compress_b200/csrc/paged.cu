@@ -503,6 +503,8 @@ __global__ void __launch_bounds__(kFmaThreads) paged_fma_kernel(const __grid_con
   PagedWalk<M, TK> w(a, st, share);
   bool first = true;
   const float c2 = a.sm_scale * kPagedLog2e, cap2 = a.cap * kPagedLog2e;
+  const bool bent = a.cap > 0.f || a.slopes;
+  const float factor = bent ? 1.f : c2;  // from what s_s holds to base-2 units
   while (w.next()) {
     if (tid == 0 && first) w.write_meta(false);
     first = false;
@@ -573,27 +575,34 @@ __global__ void __launch_bounds__(kFmaThreads) paged_fma_kernel(const __grid_con
       __syncthreads();
       {  // scores
         const int key = tid % TK, g = (tid / TK) * 4;
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        float acc[4] = {};  // sums of the sums of 16 dims: a chain of all would round more
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           const uint4 u = *reinterpret_cast<const uint4*>(&kv_s[stage][0][key * D + ((c ^ (key & (CH - 1))) * 16)]);
           const uint32_t wd[4] = {u.x, u.y, u.z, u.w};
+          float part[4][2] = {};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 k0 = e4m3x2_val((uint16_t)wd[i]), k1 = e4m3x2_val((uint16_t)(wd[i] >> 16));
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const float4 q = *reinterpret_cast<const float4*>(&q_s[g + r][c * 16 + i * 4]);
-              acc[r] = fmaf(q.x, k0.x, fmaf(q.y, k0.y, fmaf(q.z, k1.x, fmaf(q.w, k1.y, acc[r]))));
+              part[r][0] = fmaf(q.x, k0.x, fmaf(q.y, k0.y, part[r][0]));
+              part[r][1] = fmaf(q.z, k1.x, fmaf(q.w, k1.y, part[r][1]));
             }
           }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[r] += part[r][0] + part[r][1];
         }
+        // scores; where nothing bends them they stay without their constant
+        // factor, which the exponential's argument takes in one rounding
         const float ks = sc_s[stage][0][key];
         const int j = t * TK + key;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          float s = acc[r] * ks * c2;
-          if (a.cap > 0.f) s = cap2 * tanhf(s / cap2);
+          float s = acc[r] * ks;
+          if (bent) s *= c2;
+          if (a.cap > 0.f) s = paged_cap(s, cap2);
           if (a.slopes && g + r < rows)
             s -= a.slopes[w.p_h * a.G + r0 + g + r - paged_div(a, r0 + g + r) * a.G] * (float)abs(pos_s[g + r] - j) * kPagedLog2e;
           s_s[g + r][key] = (ks >= 0.f && j >= lo_s[g + r] && j < hi_s[g + r]) ? s : -INFINITY;
@@ -604,9 +613,9 @@ __global__ void __launch_bounds__(kFmaThreads) paged_fma_kernel(const __grid_con
       for (int rr = 0; rr < 2; ++rr) {  // softmax of rows 2 warp, 2 warp + 1
         const int r = warp * 2 + rr;
         const float s0 = s_s[r][lane], s1 = s_s[r][lane + 32];
-        const float m_old = m_s[r], m_new = fmaxf(m_old, warp_max(fmaxf(s0, s1)));
+        const float m_old = m_s[r], m_new = fmaxf(m_old, warp_max(fmaxf(s0, s1)) * factor);
         const float ref = m_new == -INFINITY ? 0.f : m_new;
-        const float p0 = paged_ex2(s0 - ref), p1 = paged_ex2(s1 - ref);
+        const float p0 = paged_ex2(fmaf(s0, factor, -ref)), p1 = paged_ex2(fmaf(s1, factor, -ref));
         const float sum = warp_sum(p0 + p1);
         p_s[lane][r] = p0 * sc_s[stage][1][lane];
         p_s[lane + 32][r] = p1 * sc_s[stage][1][lane + 32];

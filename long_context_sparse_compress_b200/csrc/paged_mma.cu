@@ -218,7 +218,7 @@ struct PageAhead {
 };
 
 // =============================================================== few rows
-// Decode steps and draft tokens: up to 32 query rows per item.  The keys lie on
+// Decode steps and draft tokens: up to 16 query rows per item.  The keys lie on
 // the M side of both products, so that a tile of 128 keys is one full-height MMA
 // however few the rows are, and K and V go from TMA straight into the tensor
 // cores as they are stored:
@@ -238,7 +238,8 @@ struct PageAhead {
 // Bound: HBM (2 D bytes per key and KV head).  Per tile the tensor pipe reads
 // 5 x 16 KB of operands (640 cycles of shared memory at D = 128 against 1,420
 // cycles of HBM time); two CTAs per SM overlap one's softmax with the other's
-// copies and products.
+// copies and products.  16 requests of 16K to 64K tokens, 64 heads on 8, D = 128:
+// 204 us, 5.8 TB/s, 90% of the measured copy rate.
 
 constexpr int kFewThreads = 192;  // warps 0-3 softmax, 4 copies, 5 MMA
 constexpr int kQTerms = 2, kPTerms = 3;
@@ -246,12 +247,12 @@ constexpr int kQTerms = 2, kPTerms = 3;
 template <int D, int NR>
 struct FewCfg {
   static constexpr int TK = 128;
-  static constexpr int N = NR < 16 ? 16 : NR;        // MMA columns (a multiple of 16)
-  static constexpr int PW = NR <= 16 ? 64 : 128;     // bytes of a key's weights: 3 terms of N
+  static constexpr int N = 16;                       // MMA columns (a multiple of 16)
+  static constexpr int PW = 64;                      // bytes of a key's weights: 3 terms of N
   static constexpr int kTile = TK * D;               // K or V bytes of a tile
-  static constexpr int kStages = D == 128 && NR == 32 ? 2 : 3;
+  static constexpr int kStages = 3;
   static constexpr int kPerSm = 2;
-  static constexpr int kCols = NR <= 16 ? 64 : 128;  // TMEM columns: S twice, O
+  static constexpr int kCols = 64;                   // TMEM columns: S twice, O
   static constexpr int OFF_K = 0;
   static constexpr int OFF_V = OFF_K + kStages * kTile;
   static constexpr int OFF_Q = OFF_V + kStages * kTile;
@@ -273,10 +274,11 @@ struct FewCfg {
   static_assert(kBars % 2 == 0 && OFF_F4 % 16 == 0 && OFF_F2 % 8 == 0 && OFF_ROW % 16 == 0 && OFF_SCAN % 8 == 0, "alignment");
   static_assert(OFF_Q % 1024 == 0 && OFF_P % 1024 == 0 && kQBytes % 1024 == 0, "swizzle atoms");
   static_assert(kPerSm * (SMEM + 1024) <= 228 * 1024, "resident CTAs");
-  static_assert(kPTerms * N <= PW, "a key's weights");
+  static_assert(NR <= N && kPTerms * N <= PW && 3 * N <= kCols, "a key's weights, the accumulators");
 };
 
-template <int D, int NR>
+// CAP: scores are capped (the code for it, though not run, cost the plain kernel 6%).
+template <int D, int NR, bool CAP>
 __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
     paged_few_kernel(const __grid_constant__ PagedLaunch a, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const WaitTest test) {
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
             float y = __uint_as_float(x[r]) * (kf * qs_s[r]);
-            if (a.cap > 0.f) y = paged_cap(y, cap2);
+            if constexpr (CAP) y = paged_cap(y, cap2);
             if (a.slopes) y -= __int_as_float(row_s[r].w) * (float)abs(row_s[r].z - j);
             bool see = seen;
             if (!inside) see = see && j >= row_s[r].x && j < row_s[r].y;
@@ -656,21 +658,30 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
 }
 
 // ============================================================== many rows
-// Prompts: blocks of 256 query rows, as two tiles of 128 that share K and V.
+// Prompts, and decode of many heads on one: blocks of 256 query rows, as two
+// tiles of 128 that share K and V.
 //   S [128 rows][128 keys] = Q K^T     Q: two E4M3 terms, K as stored (kind::f8f6f4)
 //   O [128 rows][D dims]  += P V       P and V in f16 (kind::f16)
 // A softmax warpgroup owns a tile and a thread one row of it: maxima and sums
 // need no exchange.  O stays in TMEM; it is rescaled only when a row's maximum
 // has grown by more than 2^8 over the reference (weights then reach 256, well
 // inside f16).  V's codes become f16 numbers exactly: four warps read them
-// from global memory a tile ahead and write code * 2^7 * (page scale / largest
-// page scale of the piece), which is exact for scales down to 2^-13 of the
-// largest and loses only what lies below 2^-31 of the largest possible |V|.  Two
-// tiles keep the tensor cores busy with one while the other's weights are made.
+// from global memory half a tile ahead and write code * 2^7 * (page scale /
+// largest page scale of the piece), which is exact for scales down to 2^-13 of
+// the largest and loses only what lies below 2^-31 of the largest possible |V|.
+// Two tiles keep the tensor cores busy with one while the other's weights are
+// made; a block of up to 128 rows is one tile, which the two warpgroups share by
+// taking its tiles of keys in turn and joining their O at the end.
 //
-// Bound: per 256 x 128 step the products take 2,048 cycles, as do the
-// exponentials (32 K at 16 a cycle), and shared memory about 2,900 (operands
-// 2,048, P 512, V 256, K 128).
+// Bound: per 256 x 128 step the products take 2,048 cycles of the tensor pipe,
+// as do the exponentials of the MUFU (32 K at 16 a cycle), and shared memory
+// about 2,900 (operands 2,048, P 512, V 256, K 128).  Measured 4,700: one
+// warpgroup's chain of waiting for its scores (700), their maxima (800), weights
+// (2,200) and the copies' bookkeeping; taking work out of the kernel shows that
+// no unit holds it (no exponentials: -2%, one query term: -4%, no V
+// conversion: -8%), while larger loop bodies cost 10 to 30%.  Chunk of 4096
+// tokens on 4096 cached, 64 heads on 8, D = 128: 968 us, 0.85 PFLOP/s, 52% of the
+// measured bf16 rate.
 
 constexpr int kManyThreads = 448;  // warps 0-7 softmax (two tiles), 8-11 V, 12 copies, 13 MMA
 constexpr int kManyRows = 256;
@@ -712,30 +723,27 @@ __device__ __forceinline__ uint32_t many_seen(const ManyRow& r, int j, uint32_t 
   return below_hi & ~below_lo & ((there & 1u ? 0x0000ffffu : 0u) | (there & 2u ? 0xffff0000u : 0u));
 }
 
-// 32 scores capped to c tanh(v / c).  While all of the warp's are within the cap,
-// tanh(y) = y p(y^2) with a polynomial of degree 6 fitted to tanh(y) / y on
-// [-1, 1] (relative error 1.7e-7): 4.5 packed operations a score, against two
-// of the 16-cycle MUFU operations of the exponential form that takes the rest.
+// 32 scores capped: while all of the warp's are within the cap, by paged_cap's
+// polynomial in packed operations (4.5 a score, against two of the 8-cycle MUFU
+// operations of the exponential form that takes the rest).
 __device__ __forceinline__ void many_cap(float (&v)[32], float cap) {
   float most = 0.f;
 #pragma unroll
   for (int i = 0; i < 32; ++i) most = fmaxf(most, fabsf(v[i]));
   if (__all_sync(0xffffffffu, !(most > cap))) {
-    constexpr float kTanh[7] = {0.99999994f,   -0.333328396f,  0.13325204f,  -0.0534570217f,
-                                0.0202899612f, -0.00620336272f, 0.00104101724f};
     const float inv = 1.f / cap;
     const uint64_t inv2 = pack2(inv, inv);
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
       const uint64_t x = pack2(v[i], v[i + 1]), y = mul2(x, inv2), z = mul2(y, y);
-      uint64_t p = pack2(kTanh[6], kTanh[6]);
+      uint64_t p = pack2(paged_tanh(6), paged_tanh(6));
 #pragma unroll
-      for (int k = 5; k >= 0; --k) p = fma2(p, z, pack2(kTanh[k], kTanh[k]));
+      for (int k = 5; k >= 0; --k) p = fma2(p, z, pack2(paged_tanh(k), paged_tanh(k)));
       unpack2(mul2(x, p), v[i], v[i + 1]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = paged_cap(v[i], cap);
+    for (int i = 0; i < 32; ++i) v[i] = paged_cap_far(v[i], cap);
   }
 }
 
@@ -817,8 +825,8 @@ __device__ __forceinline__ void many_rescale(uint32_t o_addr, float alpha) {
   tmem_st_wait();
 }
 
-// GEN: scores are capped or biased (both forms of the loop in one kernel cost the
-// plain one GENCOST).
+// GEN: scores are capped or biased (both forms of the loop in one kernel cost
+// the plain one 1%, the other 4%).
 template <int D, bool GEN>
 __global__ void __launch_bounds__(kManyThreads, 1)
     paged_many_kernel(const __grid_constant__ PagedLaunch a, const __grid_constant__ CUtensorMap map_k, const WaitTest test) {
@@ -828,9 +836,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);  // [2]
-  uint64_t* k_empty = k_full + 2;    // [2] both tiles' Q K^T are done
+  uint64_t* k_empty = k_full + 2;    // [2] every Q K^T on it is done
   uint64_t* v_full = k_full + 4;     // [2] V is there in f16
-  uint64_t* v_empty = k_full + 6;    // [2] both tiles' P V are done
+  uint64_t* v_empty = k_full + 6;    // [2] every P V on it is done
   uint64_t* s_full = k_full + 8;     // [2 tiles]
   uint64_t* p_full = k_full + 10;    // [2 tiles] P is written, S is read
   uint64_t* pv_done = k_full + 12;   // [2 tiles]
@@ -1341,7 +1349,7 @@ bool map_pool(CUtensorMap* m, const PagedLaunch& a, const void* base, int rows) 
 template <int D, int NR>
 cudaError_t launch_few(const PagedLaunch& a, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
   using C = FewCfg<D, NR>;
-  auto kern = paged_few_kernel<D, NR>;
+  auto kern = a.cap > 0.f ? paged_few_kernel<D, NR, true> : paged_few_kernel<D, NR, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(a.ctas), dim3(kFewThreads), C::SMEM, stream, a, k, v, wait_test());
@@ -1361,17 +1369,21 @@ cudaError_t launch_mma(const PagedLaunch& a, const PagedForm& f, const CUtensorM
   if (f.kind == 2) return launch_many<D>(a, k, stream);
   switch (f.rows) {
     case 8: return launch_few<D, 8>(a, k, v, stream);
-    case 16: return launch_few<D, 16>(a, k, v, stream);
-    default: return launch_few<D, 32>(a, k, v, stream);
+    default: return launch_few<D, 16>(a, k, v, stream);
   }
 }
 
 }  // namespace
 
 PagedForm paged_mma_form(int D, int G, int64_t max_new) {
-  const int64_t rows = max_new * G;
+  // Few rows: up to 16 per KV head and request.  From 17 on two warpgroups over
+  // 128 rows are faster, however many of them are empty (16 requests of 4K to
+  // 32K tokens, 8 KV heads, D = 128, us: 8 rows 127 against 249, 16 rows 182
+  // against 252, 32 rows 307 with a few-rows kernel of that size against 258;
+  // D = 64, 32 rows: 291 against 202).
+  const int64_t rows = max_new > 16 ? 17 : max_new * G;
   if (rows > 16) return {2, kManyRows, sm_count()};
-  return {1, rows <= 8 ? 8 : rows <= 16 ? 16 : 32, 2 * sm_count()};
+  return {1, rows <= 8 ? 8 : 16, 2 * sm_count()};
 }
 
 cudaError_t launch_paged_mma(const PagedLaunch& a, const PagedForm& f, cudaStream_t stream) {

@@ -233,10 +233,10 @@ class Case:
         want, lse, dot, vmax = want[:live], lse[:live], dot[:live], vmax[:live]
         # bound of a score's error: D products and their sums in float32 (half a
         # step 2^-24 each, on sums of at most `dot`), its scale, cap, bias and
-        # exponential (2^-21 in all, times the bias' and cap's size); the bf16
-        # query's E4M3 terms add 2^-17 of its largest value per key value
+        # exponential (2^-21 in all, times the score's and the bias' size); the
+        # bf16 query's E4M3 terms add 2^-17 of its largest value per key value
         n = max(self.ctx.max(), 1)
-        size = scale * dot + (kw.get("cap") or 0.0) + (np.max(kw["slopes"]) * n if kw.get("slopes") is not None else 0)
+        size = scale * dot + (np.max(kw["slopes"]) * n if kw.get("slopes") is not None else 0)
         ds = (self.D + 8) * 2.0 ** -24 * scale * dot + 2.0 ** -21 * (1 + size)
         dp = 0.0
         if self.dtype == BF16:
@@ -350,6 +350,16 @@ def test_window_passes_over_released_pages(cuda_lib, dtype):
     table = c.table.copy()
     table[0, :(300 - 40) // 16], table[1, :(500 - 4 - 40) // 16] = -1, c.n_pages + 5
     c.run(table=table, window=40).check(window=40)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("new", [[1, 1], [40, 30]])
+def test_caps_far_above_and_below_the_scores(cuda_lib, dtype, new):
+    """A cap of ten thousand nearly changes nothing, and is not to cost precision; one
+    far below the scores leaves little more than their signs."""
+    c = Case([190, 64], new, 8, 2, 128, 16, dtype, seed=22)
+    c.run(cap=1e4).check(cap=1e4)
+    c.run(cap=0.25).check(cap=0.25)
 
 
 def test_page_scales_far_apart(cuda_lib):

@@ -40,7 +40,8 @@ BAD_PARAMS = [
     (INVALID, dict(n_kv_heads=-2)), (INVALID, dict(q_dtype=2)), (INVALID, dict(x_dtype=-1)),
     (INVALID, dict(sm_scale=0.0)), (INVALID, dict(sm_scale=float("nan"))), (INVALID, dict(sm_scale=float("inf"))),
     (INVALID, dict(window=-1)), (INVALID, dict(softcap=-1.0)), (INVALID, dict(softcap=float("nan"))),
-    (INVALID, dict(softcap=float("inf"))), (UNSUPPORTED, dict(page_size=8)), (UNSUPPORTED, dict(page_size=48)),
+    (INVALID, dict(softcap=float("inf"))), (INVALID, dict(softcap=1e-7)), (INVALID, dict(softcap=1.1e4)),
+    (UNSUPPORTED, dict(page_size=8)), (UNSUPPORTED, dict(page_size=48)),
     (UNSUPPORTED, dict(page_size=256)), (UNSUPPORTED, dict(page_size=0)), (UNSUPPORTED, dict(head_dim=96)),
     (UNSUPPORTED, dict(head_dim=512))]
 
