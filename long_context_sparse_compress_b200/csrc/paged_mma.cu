@@ -679,7 +679,8 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
 // warpgroup's chain of waiting for its scores (700), their maxima (800), weights
 // (2,200) and the copies' bookkeeping; taking work out of the kernel shows that
 // no unit holds it (no exponentials: -2%, one query term: -4%, no V
-// conversion: -8%), while larger loop bodies cost 10 to 30%.  Chunk of 4096
+// conversion: -8%), while larger loop bodies cost 10 to 30% and twice the
+// softmax warps 46%.  Chunk of 4096
 // tokens on 4096 cached, 64 heads on 8, D = 128: 968 us, 0.85 PFLOP/s, 52% of the
 // measured bf16 rate.
 
