@@ -674,51 +674,90 @@ __global__ void __launch_bounds__(kFmaThreads) paged_fma_kernel(const __grid_con
 }
 
 // ---------------------------------------------------------- split items
-// Joins the pieces of an item in CTA order: O = sum_i 2^(m_i - m) O_i and the
-// same for the sums.  The CTAs of the item's second piece do it, a warp for a
-// row: a lane per piece for the maxima and sums, then 4 (D = 64: 2) dims per
-// lane over the pieces.
-constexpr int kCombineRows = 8;
+// Joins the pieces of an item: O = sum_i 2^(m_i - m) O_i and the same for the
+// sums.  The CTAs of the item's second piece do it.  A row is a warp's, or,
+// where an item has few rows (and then often many pieces: one per CTA of the
+// GPU for one long request), that of 2, 4 or 8 warps that share its pieces and
+// join theirs in shared memory; which, follows from the item alone, so that the
+// order of every sum is fixed.  A lane per piece for the maxima and sums, then 4
+// (D = 64: 2) dims per lane over the pieces, four in flight.
+constexpr int kCombineWarps = 8, kCombineY = 32;
 
 template <int D>
-__global__ void __launch_bounds__(kCombineRows * 32) paged_combine_kernel(PagedLaunch a, int M) {
+__global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(PagedLaunch a, int M) {
   grid_dep_wait();
   constexpr int VPL = D / 32;
-  const int c = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * kCombineRows + threadIdx.x / 32;
+  __shared__ float2 ml_s[kCombineWarps];
+  __shared__ float o_s[kCombineWarps][D];
+  const int c = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int32_t* m = a.meta + 8 * (int64_t)c;
   const int b = m[0], h = m[1], mt = m[2], c0 = m[3], c1 = m[4];
-  if (b < 0 || c != c0 + 1) return;
+  if (b < 0 || c != c0 + 1) return;  // the same for the whole CTA
   const PagedSeq s = paged_seq(a, b);
-  if (r >= min(M, s.n * a.G - mt * M)) return;
-  // the place of piece i's row
-  auto place = [&](int i) { return (2 * (int64_t)i + (i == c0 ? 1 : 0)) * M + r; };
+  const int rows = min(M, s.n * a.G - mt * M);
+  int per_cta = 1;  // rows of a CTA
+  while (per_cta < kCombineWarps && per_cta * (int)gridDim.y < rows) per_cta *= 2;
+  const int share = kCombineWarps / per_cta, sub = warp % share, r = blockIdx.y * per_cta + warp / share;
   float top = -INFINITY, l = 0.f, o[VPL] = {};
-  for (int i0 = c0; i0 <= c1; i0 += 32) {  // 32 pieces at a time
-    const int n = min(32, c1 - i0 + 1);
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (lane < n) ml = *reinterpret_cast<const float2*>(a.part_ml + place(i0 + lane) * 2);
-    const float high = fmaxf(top, warp_max(ml.x)), ref = high == -INFINITY ? 0.f : high;
-    const float old = paged_ex2(top - ref), f = paged_ex2(ml.x - ref);
-    top = high;
-    l = fmaf(l, old, warp_sum(ml.y * f));
+  if (r < rows) {
+    // the place of the row in piece i (the first is its CTA's last)
+    auto place = [&](int i) { return (2 * (int64_t)i + (i == c0 ? 1 : 0)) * M + r; };
+    for (int i0 = c0 + sub; i0 <= c1; i0 += 32 * share) {  // 32 of this warp's pieces at a time
+      const int mine = i0 + lane * share;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (mine <= c1) ml = *reinterpret_cast<const float2*>(a.part_ml + place(mine) * 2);
+      const float high = fmaxf(top, warp_max(ml.x)), ref = high == -INFINITY ? 0.f : high;
+      const float old = paged_ex2(top - ref), f = paged_ex2(ml.x - ref);
+      top = high;
+      l = fmaf(l, old, warp_sum(ml.y * f));
 #pragma unroll
-    for (int k = 0; k < VPL; ++k) o[k] *= old;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float fi = __shfl_sync(0xffffffffu, f, i);
-      const float* p = a.part_o + place(i0 + i) * D + lane * VPL;
-      float v[VPL];
-      if constexpr (VPL == 4) {
-        const float4 u = *reinterpret_cast<const float4*>(p);
-        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
-      } else {
-        const float2 u = *reinterpret_cast<const float2*>(p);
-        v[0] = u.x, v[1] = u.y;
+      for (int k = 0; k < VPL; ++k) o[k] *= old;
+      const int n = min(32, ((c1 - i0) >> (31 - __clz(share))) + 1);  // share: a power of two
+#pragma unroll 1
+      for (int i = 0; i < n; i += 4) {  // four in flight, the last one again where there are fewer
+        float v[4][VPL], fi[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int piece = min(i + q, n - 1);
+          fi[q] = __shfl_sync(0xffffffffu, f, piece);
+          const float* p = a.part_o + place(i0 + piece * share) * D + lane * VPL;
+          if constexpr (VPL == 4) {
+            const float4 u = *reinterpret_cast<const float4*>(p);
+            v[q][0] = u.x, v[q][1] = u.y, v[q][2] = u.z, v[q][3] = u.w;
+          } else {
+            const float2 u = *reinterpret_cast<const float2*>(p);
+            v[q][0] = u.x, v[q][1] = u.y;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int k = 0; k < VPL; ++k) o[k] = i + q < n ? fmaf(fi[q], v[q][k], o[k]) : o[k];
       }
-#pragma unroll
-      for (int k = 0; k < VPL; ++k) o[k] = fmaf(fi, v[k], o[k]);
     }
   }
+  if (share > 1) {
+    if (lane == 0) ml_s[warp] = make_float2(top, l);
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) o_s[warp][lane * VPL + k] = o[k];
+    __syncthreads();
+    if (sub != 0) return;
+    float high = top;
+    for (int i = 1; i < share; ++i) high = fmaxf(high, ml_s[warp + i].x);
+    const float ref = high == -INFINITY ? 0.f : high, own = paged_ex2(top - ref);
+    l *= own;
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) o[k] *= own;
+    for (int i = 1; i < share; ++i) {
+      const float2 ml = ml_s[warp + i];
+      const float f = paged_ex2(ml.x - ref);
+      l = fmaf(ml.y, f, l);
+#pragma unroll
+      for (int k = 0; k < VPL; ++k) o[k] = fmaf(o_s[warp + i][lane * VPL + k], f, o[k]);
+    }
+    top = high;
+  }
+  if (r >= rows) return;
   int64_t at;
   const float f = paged_close(a, s, h, mt * M + r, top, l, lane == 0, &at);
 #pragma unroll
@@ -782,7 +821,7 @@ cudaError_t launch_paged_attn(const PagedLaunch& a, const PagedForm& f, cudaStre
   cudaError_t e = f.kind ? launch_paged_mma(a, f, stream)
                   : a.D == 128 ? launch_fma<128>(a, stream) : launch_fma<64>(a, stream);
   if (e != cudaSuccess || a.ctas == 1) return e;
-  const dim3 grid(a.ctas, f.rows / kCombineRows), block(kCombineRows * 32);
+  const dim3 grid(a.ctas, f.rows / 4 < kCombineY ? f.rows / 4 : kCombineY), block(kCombineWarps * 32);
   return a.D == 128 ? launch_pdl(paged_combine_kernel<128>, grid, block, 0, stream, a, f.rows)
                     : launch_pdl(paged_combine_kernel<64>, grid, block, 0, stream, a, f.rows);
 }
