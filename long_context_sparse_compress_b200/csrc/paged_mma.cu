@@ -928,51 +928,51 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const bool shared = w.rows() <= 128;  // both warpgroups on one tile of rows
       if (!(go = wait(q_full, (uint32_t)pieces & 1u))) break;
       ++pieces;
-      const int T = keys.t1 - keys.t0, last = shared ? 0 : 1;
-      // Per tile of keys: Q K^T of the next, P V of the last, for each tile of
-      // rows or, where there is one, for the warpgroups in turn.
-      for (int i = 0; go && i <= T; ++i) {
-        const int s = n & 1;
-        if (i < T && !(go = wait(&k_full[s], (uint32_t)(n >> 1) & 1u))) break;
+      // Per warpgroup: Q K^T of its next tile of keys as soon as its scores are
+      // read, then P V of its last one (the tile before, or, where the
+      // warpgroups take the tiles in turn, the one before that).
+      const int T = keys.t1 - keys.t0, last = shared ? 0 : 1, lag = shared ? 2 : 1;
+      for (int i = 0; go && i < T + lag; ++i) {
+        const int s = (n + i) & 1;
+        if (i < T && !(go = wait(&k_full[s], (uint32_t)((n + i) >> 1) & 1u))) break;
         for (int e = 0; e <= last; ++e) {
-          const int gq = shared ? i & 1 : e, gp = shared ? gq ^ 1 : e;
-          if (!shared && i > 0 && !(go = wait(&p_full[gp], (uint32_t)(cnt[gp] - 1) & 1u))) break;
+          const int g = shared ? i & 1 : e;
+          if (i >= lag && !(go = wait(&p_full[g], (uint32_t)(cnt[g] - 1) & 1u))) break;
           if (i < T) {
             tc_fence_after();
             if (elect_one()) {
-              const uint32_t ka = smem_u32(sm + C::OFF_K + s * C::kK), qt = qa + (shared ? 0 : 2 * e) * C::kQTerm;
+              const uint32_t ka = smem_u32(sm + C::OFF_K + s * C::kK), qt = qa + 2 * e * C::kQTerm;
 #pragma unroll
               for (int term = 0; term < kQTerms; ++term)
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k)
-                  mma_ss<1>(tmem + gq * 128, smem_desc(qt + term * C::kQTerm + k * 32, 16, 8 * D, kSwOf<D>),
+                  mma_ss<1>(tmem + g * 128, smem_desc(qt + term * C::kQTerm + k * 32, 16, 8 * D, kSwOf<D>),
                             smem_desc(ka + k * 32, 16, 8 * D, kSwOf<D>), idesc_qk, k > 0 || term > 0);
-              tc_commit(&s_full[gq]);
+              tc_commit(&s_full[g]);
               if (e == last) tc_commit(&k_empty[s]);
             }
             __syncwarp();
           }
-          if (i > 0) {
-            const int m = n - 1, b = m & 1;
-            if (shared && !(go = wait(&p_full[gp], (uint32_t)(cnt[gp] - 1) & 1u))) break;
+          if (i >= lag) {
+            const int m = n + i - lag, b = m & 1;
             if (e == 0 && !(go = wait(&v_full[b], (uint32_t)(m >> 1) & 1u))) break;
             tc_fence_after();
             if (elect_one()) {
-              const uint32_t pa = smem_u32(sm + C::OFF_P + gp * C::kP), va = smem_u32(sm + C::OFF_V + b * C::kV);
-              const bool acc = i > (shared ? 2 : 1);
+              const uint32_t pa = smem_u32(sm + C::OFF_P + g * C::kP), va = smem_u32(sm + C::OFF_V + b * C::kV);
+              const bool acc = i >= 2 * lag;  // not the warpgroup's first tile
 #pragma unroll
               for (int k = 0; k < TK / 16; ++k)
-                mma_ss<0>(tmem + 256 + gp * 128, smem_desc(pa + (k / 4) * (128 * 128) + (k % 4) * 32, 16, 1024, kSw128),
+                mma_ss<0>(tmem + 256 + g * 128, smem_desc(pa + (k / 4) * (128 * 128) + (k % 4) * 32, 16, 1024, kSw128),
                           smem_desc(va + k * 16 * 128, TK * 128, 1024, kSw128), idesc_pv, acc || k > 0);
-              tc_commit(&pv_done[gp]);
+              tc_commit(&pv_done[g]);
               if (e == last) tc_commit(&v_empty[b]);
             }
             __syncwarp();
           }
-          if (i < T) ++cnt[gq];
+          if (i < T) ++cnt[g];
         }
-        if (go && i < T) ++n;
       }
+      n += T;
     }
     if (lane == 0) {
       tc_commit(drain);
