@@ -62,6 +62,10 @@ __device__ __forceinline__ void st_shared16(uint32_t at, uint32_t x, uint32_t y,
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
+__device__ __forceinline__ void st_shared8(uint32_t at, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
+}
+
 // Two float32 operations in one instruction.
 __device__ __forceinline__ uint64_t pack2(float x, float y) {
   uint64_t v;
@@ -696,11 +700,12 @@ struct ManyCfg {
   static constexpr int kV = TK * D * 2;
   static constexpr int kP = 128 * TK * 2;
   static constexpr int OFF_Q = 0;                     // [2 tiles][2 terms]
+  static constexpr int OFF_SWAP = OFF_Q + 2 * kQTerm; // float [2 warpgroups][128], where a block has no second tile
   static constexpr int OFF_K = OFF_Q + 4 * kQTerm;    // [2]
   static constexpr int OFF_V = OFF_K + 2 * kK;        // [2]
   static constexpr int OFF_P = OFF_V + 2 * kV;        // [2 tiles]
   static constexpr int OFF_BAR = OFF_P + 2 * kP;
-  static constexpr int kBars = 19;
+  static constexpr int kBars = 21;
   static constexpr int OFF_ML = OFF_BAR + (kBars + 1) / 2 * 16;  // float2 [128]: the second warpgroup's maxima and sums
   static constexpr int OFF_SCAN = OFF_ML + 128 * 8;  // PagedScratch
   static constexpr int OFF_VREF = OFF_SCAN + (int)sizeof(PagedScratch);    // int: largest V scale of the piece (bits)
@@ -760,7 +765,7 @@ __device__ __forceinline__ void many_bias(float (&v)[32], const ManyRow& r, int 
   }
 }
 
-// A row's largest score over a tile, in base-2 units; lanes of .. of + 7 of
+// A row's largest score over the keys h0 .. h1 of a tile, in base-2 units; lanes of .. of + 7 of
 // `ks` hold the K scales of the tile's 16-key groups (-1: not there).  Three forms:
 //   kPlain:  every row of the warp sees every key, no cap, no bias: the largest
 //            raw product of each page, times its factor
@@ -773,10 +778,10 @@ __device__ __forceinline__ void many_bias(float (&v)[32], const ManyRow& r, int 
 enum ManyForm { kPlain, kMasked, kScores };
 template <ManyForm F>
 __device__ __forceinline__ float many_top(const PagedLaunch& a, const ManyRow& r, float cap2, float ks, int of, int j0,
-                                          bool inside, uint32_t s_addr) {
+                                          bool inside, uint32_t s_addr, int h0, int h1) {
   float top = -INFINITY;
 #pragma unroll 1
-  for (int h = 0; h < 128; h += 32) {
+  for (int h = h0; h < h1; h += 32) {
     uint32_t x[32];
     tmem_ld(s_addr + h, x);
     const float k0 = __shfl_sync(0xffffffffu, ks, of + (h >> 4)), k1 = __shfl_sync(0xffffffffu, ks, of + (h >> 4) + 1);
@@ -848,6 +853,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   uint64_t* piece_done = k_full + 16;
   uint64_t* drain = k_full + 17;
   uint64_t* ml_full = k_full + 18;   // the second warpgroup's part of a shared block of rows
+  uint64_t* swap_full = k_full + 19;  // [2 warpgroups]
   float2* ml_s = reinterpret_cast<float2*>(sm + C::OFF_ML);
   volatile int* vref_s = reinterpret_cast<volatile int*>(sm + C::OFF_VREF);
   uint32_t* tm_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_TM);
@@ -860,6 +866,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 4), mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4), mbar_init(&pv_done[i], 1);
+      mbar_init(&swap_full[i], 4);
     }
     mbar_init(q_full, 8);
     mbar_init(ref_full, 4);
@@ -1086,67 +1093,88 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const uint32_t lane_base = (uint32_t)((warp % 4) * 32) << 16;
     const uint32_t s_addr = tmem + g * 128 + lane_base, o_addr = tmem + 256 + g * 128 + lane_base;
     bool ok = true;
-    int cnt = 0, pieces = 0, merges = 0;
+    float* swap_s = reinterpret_cast<float*>(sm + C::OFF_SWAP) + g * 128;
+    int cnt = 0, pieces = 0, merges = 0, swaps = 0;
     while (ok && w.next()) {
       const PieceKeys<M, TK> keys(a, w);
       const int rows = w.rows();
       // Up to 128 rows are one tile that both warpgroups work on, taking its
       // tiles of keys in turn, each with its own maxima, sums and O.
       const bool shared = rows <= 128;
-      const int r_in = (shared ? 0 : g * 128) + row_in, r0 = w.p_mt * M + r_in - row_in;
+      // Up to 64 rows lie in the tile twice, and a row's two threads take a half of
+      // each tile's keys; they agree on its maximum, and the first has its O.  Half
+      // the scores a thread where they are long work (capped or biased: a million
+      // tokens for 64 heads on one 157 -> 131 us, five draft tokens of 8 heads 186 ->
+      // 178); plain ones gain 1% with 32 rows and lose 2% on a prompt's chunk.
+      const bool split = GEN && rows <= 64;
+      const int side = split ? row_in / 64 : 0, t_row = split ? row_in % 64 : row_in;
+      const int h0 = 64 * side, h1 = split ? h0 + 64 : 128;
+      const int base = shared ? 0 : g * 128, r_in = base + t_row, row = w.p_mt * M + r_in;
       const bool mine = r_in < rows;
+      auto swapped = [&](float x, float* y) {  // the other thread's x
+        swap_s[row_in] = x;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&swap_full[g]);
+        const bool there = wait(&swap_full[g], (uint32_t)swaps++ & 1u);
+        *y = swap_s[row_in ^ 64];
+        return there;
+      };
       ManyRow r = {0, INT_MAX, 1 << 30, 0.f, 0.f};  // a row that is not there sees everything and bears no bias
       if (mine) {
-        const int i = paged_div(a, r0 + row_in);
+        const int i = paged_div(a, row);
         paged_span(a, w.p_s, paged_prefix(a, w.p_b), i, &r.lo, &r.hi);
         r.pos = w.p_s.L - w.p_s.n + i;
         if (a.docs) r.lo = max(r.lo, a.docs[w.p_s.q0 + i]);
-        if (a.slopes) r.slope = a.slopes[w.p_h * a.G + r0 + row_in - i * a.G] * kPagedLog2e;
+        if (a.slopes) r.slope = a.slopes[w.p_h * a.G + row - i * a.G] * kPagedLog2e;
       }
       const bool work = keys.t0 < w.p_t1;
       if (work) {
-        // the tile's query terms, a thread per row: its largest magnitude (all
-        // loads in flight at once), then the codes of 16 dims at a time
+        // The tile's query terms: LPR lanes read a row together, 8 dims each (a
+        // thread per row: 32 lines a load, five draft tokens 187 against 178 us).
         {
-          constexpr int CH = D / 8;  // 16-byte chunks of a row
-          const int tok = paged_div(a, r0 + row_in);
-          const uint4* q = reinterpret_cast<const uint4*>(
-              reinterpret_cast<const uint16_t*>(a.q) + (w.p_s.q0 + tok) * a.q_stride +
-              (int64_t)(w.p_h * a.G + r0 + row_in - tok * a.G) * D);
-          uint32_t top = 0;  // two magnitudes in bf16 bits, whose order is the numbers'
-          if (mine) {
-            uint4 u[CH];
-#pragma unroll
-            for (int i = 0; i < CH; ++i) u[i] = q[i];
-#pragma unroll
-            for (int i = 0; i < CH; ++i)
-              top = __vmaxu2(top, __vmaxu2(__vmaxu2(u[i].x & 0x7fff7fffu, u[i].y & 0x7fff7fffu),
-                                           __vmaxu2(u[i].z & 0x7fff7fffu, u[i].w & 0x7fff7fffu)));
-          }
-          const uint32_t amax = max(top & 0xffffu, top >> 16);  // from 0x7f80 on: not finite
-          const int ex = amax ? (int)(amax >> 7) - 127 - 7 : 0;
-          const float f = pow2(-ex);
+          constexpr int LPR = D / 8, RPI = 32 / LPR, IT = 32 / RPI;  // lanes per row, rows per step, steps
+          const int c = lane % LPR, first = warp % 4 * 32 + lane / LPR;
           const uint32_t dst = smem_u32(sm + C::OFF_Q + 2 * g * C::kQTerm);
+          uint32_t amax = 0;  // the thread's own row's largest magnitude in bf16 bits; from 0x7f80 on: not finite
 #pragma unroll 1
-          for (int c = 0; c < CH; c += 2) {
-            uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
-            if (mine) {
-              const uint4 u0 = q[c], u1 = q[c + 1];
-              const uint32_t wd[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+          for (int i0 = 0; i0 < IT; i0 += 8) {
+            uint4 u[8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float y0 = __uint_as_float(wd[i] << 16) * f, y1 = __uint_as_float(wd[i] & 0xffff0000u) * f;
+            for (int i = 0; i < 8; ++i) {
+              const int y = first + (i0 + i) * RPI, in = base + (split ? y % 64 : y), of = w.p_mt * M + in;
+              const int tok = paged_div(a, of);
+              u[i] = ld_if(reinterpret_cast<const uint8_t*>(a.q) +
+                               2 * ((w.p_s.q0 + tok) * a.q_stride + (int64_t)(w.p_h * a.G + of - tok * a.G) * D + c * 8),
+                           in < rows);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              // two magnitudes, whose bits' order is the numbers'
+              uint32_t top = __vmaxu2(__vmaxu2(u[i].x & 0x7fff7fffu, u[i].y & 0x7fff7fffu),
+                                      __vmaxu2(u[i].z & 0x7fff7fffu, u[i].w & 0x7fff7fffu));
+#pragma unroll
+              for (int o = LPR / 2; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+              top = max(top & 0xffffu, top >> 16);
+              const uint32_t own = __shfl_sync(0xffffffffu, top, lane % RPI * LPR);
+              if (lane / RPI == i0 + i) amax = own;
+              if (shared && g == 1) continue;  // the first warpgroup lays them out
+              const float f = pow2(top ? 134 - (int)(top >> 7) : 0);
+              const uint32_t wd[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+              uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float y0 = __uint_as_float(wd[q] << 16) * f, y1 = __uint_as_float(wd[q] & 0xffff0000u) * f;
                 const uint16_t hc = e4m3x2_code(y0, y1);
                 const float2 h = e4m3x2_val(hc);
-                hi[i / 2] |= (uint32_t)hc << (16 * (i & 1));
-                lo[i / 2] |= (uint32_t)e4m3x2_code(y0 - h.x, y1 - h.y) << (16 * (i & 1));
+                hi[q / 2] |= (uint32_t)hc << (16 * (q & 1));
+                lo[q / 2] |= (uint32_t)e4m3x2_code(y0 - h.x, y1 - h.y) << (16 * (q & 1));
               }
+              const uint32_t at = dst + swz<D>(first + (i0 + i) * RPI, c * 8);
+              st_shared8(at, hi[0], hi[1]);
+              st_shared8(at + C::kQTerm, lo[0], lo[1]);
             }
-            const uint32_t at = dst + swz<D>(row_in, c * 8);
-            if (shared && g == 1) continue;  // the first warpgroup lays them out
-            st_shared16(at, hi[0], hi[1], hi[2], hi[3]);
-            st_shared16(at + C::kQTerm, lo[0], lo[1], lo[2], lo[3]);
           }
+          const int ex = amax ? (int)(amax >> 7) - 134 : 0;
           // a query that is not finite gives scores that are not numbers
           r.rf = a.sm_scale * kPagedLog2e * (amax < 0x7f80u ? pow2(ex) : NAN);
         }
@@ -1183,9 +1211,14 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           tc_fence_after();
           const bool plain = !GEN && inside;  // the products are the scores but for a factor
           float top;
-          if constexpr (GEN) top = many_top<kScores>(a, r, cap2, ks, 8 * of4, j0, inside, s_addr);
-          else if (plain) top = many_top<kPlain>(a, r, cap2, ks, 8 * of4, j0, inside, s_addr);
-          else top = many_top<kMasked>(a, r, cap2, ks, 8 * of4, j0, inside, s_addr);
+          if constexpr (GEN) top = many_top<kScores>(a, r, cap2, ks, 8 * of4, j0, inside, s_addr, h0, h1);
+          else if (plain) top = many_top<kPlain>(a, r, cap2, ks, 8 * of4, j0, inside, s_addr, h0, h1);
+          else top = many_top<kMasked>(a, r, cap2, ks, 8 * of4, j0, inside, s_addr, h0, h1);
+          if (split) {
+            float other;
+            if (!(ok = swapped(top, &other))) break;
+            top = fmaxf(top, other);
+          }
           const bool fresh = t == t_first;
           float alpha = 1.f;
           bool grown = false;
@@ -1197,7 +1230,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           }
           // P and O: the last tile's P V has read and added to them
           if (!fresh && !(ok = wait(&pv_done[g], (uint32_t)(cnt - 1) & 1u))) break;
-          if (__any_sync(0xffffffffu, grown)) {
+          if (side == 0 && __any_sync(0xffffffffu, grown)) {
             tc_fence_after();
             many_rescale<D>(o_addr, alpha);
           }
@@ -1205,7 +1238,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           const uint64_t ref2 = pack2(-ref, -ref);
           uint64_t sum2 = pack2(0.f, 0.f);
 #pragma unroll 1
-          for (int h = 0; h < 128; h += 32) {
+          for (int h = h0; h < h1; h += 32) {
             uint32_t x[32], pk[16];
             tmem_ld(s_addr + h, x);
             const float k0 = __shfl_sync(0xffffffffu, ks, 8 * of4 + (h >> 4)),
@@ -1225,7 +1258,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             const uint32_t at = prow + (h >> 6) * (128 * 128);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              st_shared16(at + swz<128>(row_in, (h & 32) * 2 + i * 16), pk[4 * i], pk[4 * i + 1], pk[4 * i + 2],
+              st_shared16(at + swz<128>(t_row, (h & 32) * 2 + i * 16), pk[4 * i], pk[4 * i + 1], pk[4 * i + 2],
                           pk[4 * i + 3]);
           }
           float s0, s1;
@@ -1238,6 +1271,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           ++cnt;
         }
         if (ok && t_first < keys.t1) ok = wait(&pv_done[g], (uint32_t)(cnt - 1) & 1u);
+        if (ok && split) {
+          float other;
+          ok = swapped(l, &other);
+          l += other;
+        }
         tc_fence_after();
       }
       if (!ok) break;
@@ -1261,13 +1299,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         ++merges;
       }
       // O (times 2^7 / vref), the row's maximum and sum
-      if (!(shared && g == 1)) {
+      if (!(shared && g == 1) && side == 0) {
         const float unit = vref * (1.f / 128.f);
         int64_t at = 0;
         const int64_t part = w.slot() * M + r_in;
         float f = unit;
         if (mine && w.whole()) {
-          f *= paged_close(a, w.p_s, w.p_h, r0 + row_in, m_ref, l, true, &at);
+          f *= paged_close(a, w.p_s, w.p_h, row, m_ref, l, true, &at);
         } else if (mine) {
           a.part_ml[part * 2] = m_ref;
           a.part_ml[part * 2 + 1] = l;
