@@ -1024,64 +1024,68 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       if (lane == 0) mbar_arrive(ref_full);
       // codes to f16 (exact) and times 2^7 scale / vref: at most 448 * 2^7
       const float inv = vref > 0.f ? __fdividef(1.f, vref) * 128.f : 0.f;
-      // A warp's 32 keys of a tile in two halves of 16 (one page each), a rolled
-      // loop over the halves: while one is converted and stored the next one's
-      // page is looked up, and its codes are asked for as soon as the registers
-      // are free.
+      // A warp's 32 keys of a tile in two halves of 16 (one page each): as soon as
+      // one is converted and stored, the codes of the next tile's are asked for in
+      // its registers, and the page of the one after that is looked up.
       constexpr int HI = IT / 2;
-      uint4 raw[HI];
-      float sc;  // the half's scale (0: not there)
-      int j = keys.t0 * TK + v * 32;  // the half's first key
+      uint4 raw[2][HI];
+      float sc[2];  // the half's scale (0: not there)
+      int32_t e[2];
+      int j = keys.t0 * TK + v * 32;  // the tile's first key of the warp
       auto entry = [&](int key) { return pages.entry(key / TK, key); };
-      auto fetch = [&](int32_t e, int key) {
-        const int64_t ph = pages.place(e);
-        sc = ld_if(a.v_scale + ph, ph >= 0, 0.f);
+      auto fetch = [&](int half, int key) {
+        const int64_t ph = pages.place(e[half]);
+        sc[half] = ld_if(a.v_scale + ph, ph >= 0, 0.f);
         const int j0 = key + rsub;
         const uint8_t* src = a.v + (ph * a.page + (j0 & (a.page - 1))) * D + c * 16;
 #pragma unroll
-        for (int i = 0; i < HI; ++i) raw[i] = ld_if(src + i * RPI * D, ph >= 0 && j0 + i * RPI < keys.hi);
+        for (int i = 0; i < HI; ++i) raw[half][i] = ld_if(src + i * RPI * D, ph >= 0 && j0 + i * RPI < keys.hi);
       };
-      fetch(entry(j), j);
-      int32_t e1 = entry(j + 16);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) e[half] = entry(j + 16 * half);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        fetch(half, j + 16 * half);
+        e[half] = entry(j + 16 * half + TK);
+      }
       const int flip = (c / 4) & 1;
       const uint32_t to = smem_u32(sm + C::OFF_V) + (c / 4) * (TK * 128);  // the 64-dim atom
 #pragma unroll 1
-      for (int u = 2 * keys.t0; u < 2 * keys.t1; ++u) {
-        const int half = u & 1, b = n & 1;
-        const int jn = half ? j - 16 + TK : j + 16;  // the next half, and the one after it
-        const int32_t e2 = entry(half ? jn + 16 : jn - 16 + TK);
-        if (half == 0 && n >= 2 && !(ok = wait(&v_empty[b], (uint32_t)((n >> 1) - 1) & 1u))) break;
-        const __half2 f = __float2half2_rn(sc * inv);
+      for (int t = keys.t0; t < keys.t1; ++t) {
+        const int b = n & 1;
+        if (n >= 2 && !(ok = wait(&v_empty[b], (uint32_t)((n >> 1) - 1) & 1u))) break;
 #pragma unroll
-        for (int i = 0; i < HI; ++i) {
-          const uint32_t wd[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-          uint32_t h[8];
+        for (int half = 0; half < 2; ++half) {
+          const __half2 f = __float2half2_rn(sc[half] * inv);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const __half2 x(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(wd[q / 2] >> (16 * (q & 1))), __NV_E4M3));
-            const __half2 y = __hmul2(x, f);
-            h[q] = *reinterpret_cast<const uint32_t*>(&y);
+          for (int i = 0; i < HI; ++i) {
+            const uint32_t wd[4] = {raw[half][i].x, raw[half][i].y, raw[half][i].z, raw[half][i].w};
+            uint32_t h[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const __half2 x(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(wd[q / 2] >> (16 * (q & 1))), __NV_E4M3));
+              const __half2 y = __hmul2(x, f);
+              h[q] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            // 16 dims are two chunks of the atom; the lanes of the second atom
+            // store theirs in the other order, so that a store covers all banks
+            const int r = v * 32 + half * 16 + i * RPI + rsub, ch = (c % 4) * 2;
+            const uint32_t at = to + b * C::kV;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const bool second = (q ^ flip) != 0;
+              st_shared16(at + swz<128>(r, (ch + (q ^ flip)) * 16), second ? h[4] : h[0], second ? h[5] : h[1],
+                          second ? h[6] : h[2], second ? h[7] : h[3]);
+            }
           }
-          // 16 dims are two chunks of the atom; the lanes of the second atom
-          // store theirs in the other order, so that a store covers all banks
-          const int r = v * 32 + half * 16 + i * RPI + rsub, ch = (c % 4) * 2;
-          const uint32_t at = to + b * C::kV;
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const bool second = (q ^ flip) != 0;
-            st_shared16(at + swz<128>(r, (ch + (q ^ flip)) * 16), second ? h[4] : h[0], second ? h[5] : h[1],
-                        second ? h[6] : h[2], second ? h[7] : h[3]);
-          }
+          fetch(half, j + 16 * half + TK);
+          e[half] = entry(j + 16 * half + 2 * TK);
         }
-        fetch(e1, jn);
-        e1 = e2;
-        j = jn;
-        if (half == 1) {
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&v_full[b]);
-          ++n;
-        }
+        j += TK;
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_full[b]);
+        ++n;
       }
       if (!(ok = named_and(2, 128, ok))) break;  // the four warps go on or stop together
     }
