@@ -1141,10 +1141,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           const uint32_t dst = smem_u32(sm + C::OFF_Q + 2 * g * C::kQTerm);
           uint32_t amax = 0;  // the thread's own row's largest magnitude in bf16 bits; from 0x7f80 on: not finite
 #pragma unroll 1
-          for (int i0 = 0; i0 < IT; i0 += 8) {
-            uint4 u[8];
+          for (int i0 = 0; i0 < IT; i0 += 4) {
+            uint4 u[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i) {
               const int y = first + (i0 + i) * RPI, in = base + (split ? y % 64 : y), of = w.p_mt * M + in;
               const int tok = paged_div(a, of);
               u[i] = ld_if(reinterpret_cast<const uint8_t*>(a.q) +
@@ -1152,7 +1152,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
                            in < rows);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i) {
               // two magnitudes, whose bits' order is the numbers'
               uint32_t top = __vmaxu2(__vmaxu2(u[i].x & 0x7fff7fffu, u[i].y & 0x7fff7fffu),
                                       __vmaxu2(u[i].z & 0x7fff7fffu, u[i].w & 0x7fff7fffu));
