@@ -700,7 +700,6 @@ struct ManyCfg {
   static constexpr int kV = TK * D * 2;
   static constexpr int kP = 128 * TK * 2;
   static constexpr int OFF_Q = 0;                     // [2 tiles][2 terms]
-  static constexpr int OFF_SWAP = OFF_Q + 2 * kQTerm; // float [2 warpgroups][128], where a block has no second tile
   static constexpr int OFF_K = OFF_Q + 4 * kQTerm;    // [2]
   static constexpr int OFF_V = OFF_K + 2 * kK;        // [2]
   static constexpr int OFF_P = OFF_V + 2 * kV;        // [2 tiles]
@@ -1030,9 +1029,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       constexpr int HI = IT / 2;
       uint4 raw[2][HI];
       float sc[2];  // the half's scale (0: not there)
-      int32_t e[2];
       int j = keys.t0 * TK + v * 32;  // the tile's first key of the warp
       auto entry = [&](int key) { return pages.entry(key / TK, key); };
+      int32_t e[2] = {entry(j), entry(j + 16)};
       auto fetch = [&](int half, int key) {
         const int64_t ph = pages.place(e[half]);
         sc[half] = ld_if(a.v_scale + ph, ph >= 0, 0.f);
@@ -1041,8 +1040,6 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 #pragma unroll
         for (int i = 0; i < HI; ++i) raw[half][i] = ld_if(src + i * RPI * D, ph >= 0 && j0 + i * RPI < keys.hi);
       };
-#pragma unroll
-      for (int half = 0; half < 2; ++half) e[half] = entry(j + 16 * half);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         fetch(half, j + 16 * half);
@@ -1097,7 +1094,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const uint32_t lane_base = (uint32_t)((warp % 4) * 32) << 16;
     const uint32_t s_addr = tmem + g * 128 + lane_base, o_addr = tmem + 256 + g * 128 + lane_base;
     bool ok = true;
-    float* swap_s = reinterpret_cast<float*>(sm + C::OFF_SWAP) + g * 128;
+    // float [128]: in P's rows from 64 on, which a split block has no use for and
+    // no other warpgroup writes (whatever P V makes of them)
+    float* swap_s = reinterpret_cast<float*>(sm + C::OFF_P + g * C::kP + 64 * 128);
     int cnt = 0, pieces = 0, merges = 0, swaps = 0;
     while (ok && w.next()) {
       const PieceKeys<M, TK> keys(a, w);

@@ -316,6 +316,27 @@ def test_prompts_with_masks(cuda_lib, dtype, mask, Hq, Hkv, D, P):
     c.run(wide=True, **kw).check(**kw)
 
 
+@pytest.mark.parametrize("cap", [0.0, 5.0])
+@pytest.mark.parametrize("Hq,Hkv,D,P", [(12, 4, 64, 16), (64, 1, 128, 128), (16, 2, 128, 32)])
+def test_packed_documents(cuda_lib, Hq, Hkv, D, P, cap):
+    """Whole prompts of packed documents, whose blocks of rows begin at later and
+    later tiles of keys; a document at a block's first and last token, one that
+    starts behind every key, and requests without documents of their own."""
+    new = [700, 1, 0, 257, 64, 1000]
+    c = Case([700, 900, 40, 300, 64, 1000], new, Hq, Hkv, D, P, BF16, seed=21)
+    rng = np.random.default_rng(3)
+    docs, every = [], (40, 1, 1, 257, 5000, 333)
+    for b, n in enumerate(new):
+        pos = int(c.ctx[b]) - n + np.arange(n)
+        docs.append(pos // every[b] * every[b])
+    docs = np.concatenate(docs + [np.zeros(c.N - sum(new), int)]).astype(np.int32)
+    docs[int(c.q_start[5]) + 256:int(c.q_start[5]) + 512] = 1 << 30
+    prefix = rng.integers(0, 400, len(new)).astype(np.int32)
+    c.run(docs=docs).check(docs=docs)
+    kw = dict(docs=docs, prefix=prefix, cap=cap, window=150)
+    c.run(**kw).check(**kw)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("new", [[1, 1, 1, 1], [70, 5, 60, 1]])
 def test_bad_pages_lengths_and_absent_requests(cuda_lib, dtype, new):
