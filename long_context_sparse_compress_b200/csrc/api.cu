@@ -254,16 +254,20 @@ bool paged_sizes(const lcsc_paged_params* p, int64_t B, int64_t n_tokens, int64_
   return B >= 1 && B <= (1 << 20) && n_tokens >= 0 && n_tokens <= ((int64_t)1 << 30) / p->n_heads && max_new >= 1;
 }
 
-PagedForm plan_paged(const lcsc_paged_params* p, int64_t max_new, Carve& cv, PagedLaunch* L) {
+PagedForm plan_paged(const lcsc_paged_params* p, int64_t B, int64_t n_tokens, int64_t max_new, Carve& cv,
+                     PagedLaunch* L) {
   const PagedForm f = paged_form(p->q_dtype, p->head_dim, p->n_heads / p->n_kv_heads, max_new);
   float* po = cv.take<float>((size_t)2 * f.ctas * f.rows * p->head_dim);
   float* pml = cv.take<float>((size_t)2 * f.ctas * f.rows * 2);
   int32_t* meta = cv.take<int32_t>((size_t)8 * f.ctas);
+  int32_t* first = nullptr;
+  if (f.kind == 2) first = cv.take<int32_t>((size_t)(n_tokens * (p->n_heads / p->n_kv_heads) / f.rows + B));
   if (L) {
     L->part_o = po;
     L->part_ml = pml;
     L->meta = meta;
     L->ctas = f.ctas;
+    L->first = first;
   }
   return f;
 }
@@ -927,7 +931,7 @@ int32_t lcsc_paged_attn_workspace_size(const lcsc_paged_params* p, int64_t B, in
   if (st) return st;
   if (!bytes || !paged_sizes(p, B, n_tokens, max_new)) return LCSC_ERR_INVALID_ARG;
   Carve cv{nullptr};
-  plan_paged(p, max_new, cv, nullptr);
+  plan_paged(p, B, n_tokens, max_new, cv, nullptr);
   *bytes = cv.used;
   return LCSC_OK;
 }
@@ -949,7 +953,7 @@ int32_t lcsc_paged_attn(const lcsc_paged_params* p, const lcsc_paged_batch* s, c
   Carve cv{reinterpret_cast<uint8_t*>(ws)};
   PagedLaunch L;
   memset(&L, 0, sizeof(L));
-  const PagedForm f = plan_paged(p, s->max_new, cv, &L);
+  const PagedForm f = plan_paged(p, s->B, s->n_tokens, s->max_new, cv, &L);
   if (!ws || !aligned16(ws) || ws_bytes < cv.used) return LCSC_ERR_WORKSPACE;
   L.q = s->q;
   L.q_stride = s->q_stride;
@@ -976,6 +980,7 @@ int32_t lcsc_paged_attn(const lcsc_paged_params* p, const lcsc_paged_batch* s, c
   L.sink = s->sink;
   L.prefix = s->prefix_len;
   L.docs = s->doc_start;
+  if (!L.docs) L.first = nullptr;
   L.sm_scale = p->sm_scale;
   L.cap = p->softcap;
   L.window = p->window;

@@ -53,6 +53,8 @@ struct PagedLaunch {
   float* part_ml;  // [2 * ctas][rows per item][2]: max (base-2 units), sum
   int32_t* meta;   // [ctas][8]
   int ctas;
+  // many rows: the earliest document start in a block of rows (paged_block), or null
+  int32_t* first;    // [n_tokens * G / 256 + B]
 };
 
 struct PagedStoreLaunch {
@@ -120,8 +122,11 @@ __device__ __forceinline__ float paged_ex2(float x) {
   return y;
 }
 
+constexpr int kPagedManyRows = 256;  // rows of a block of the many-rows kernel
+
 struct PagedSeq {
   int64_t q0;  // first row
+  int b;       // the request
   int n;       // rows' tokens (0: nothing to write)
   int L;       // length; 0: its rows get zeros
 };
@@ -134,6 +139,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedLaunch& a, int b) {
   const int n = rows_ok ? q1 - q0 : 0;
   const bool len_ok = L == 0 || (L >= n && L <= a.max_blocks * a.page);
   s.q0 = q0;
+  s.b = b;
   s.n = n;
   s.L = len_ok ? L : 0;
   if ((!rows_ok || !len_ok) && a.status) atomicOr(a.status, LCSC_DEV_BAD_LENGTH);
@@ -154,6 +160,12 @@ __device__ __forceinline__ void paged_span(const PagedLaunch& a, const PagedSeq&
 
 __device__ __forceinline__ int paged_prefix(const PagedLaunch& a, int b) { return a.prefix ? a.prefix[b] : 0; }
 
+// Number of a request's block mt among all: the requests' rows follow one
+// another, and floor(x) + ceil(y) - 1 <= floor(x + y) keeps their blocks apart.
+__device__ __forceinline__ int64_t paged_block(const PagedLaunch& a, const PagedSeq& s, int mt) {
+  return s.q0 * a.G / kPagedManyRows + s.b + mt;
+}
+
 // Tiles [t0, t1) of keys that the row block mt of M rows may see; at least one.
 template <int M, int TK>
 __device__ __forceinline__ void paged_tiles(const PagedLaunch& a, const PagedSeq& s, int prefix, int mt, int* t0,
@@ -162,6 +174,11 @@ __device__ __forceinline__ void paged_tiles(const PagedLaunch& a, const PagedSeq
   int lo, hi, x;
   paged_span(a, s, prefix, paged_div(a, mt * M), &lo, &x);
   paged_span(a, s, prefix, paged_div(a, min(rows, (mt + 1) * M) - 1), &x, &hi);
+  if constexpr (M == kPagedManyRows) {
+    // An item's units are the tiles that its documents leave (packed documents
+    // under a prefix, 5 requests of 11 to 3001 tokens: 226 -> 195 us).
+    if (a.first && s.L > 0) lo = min(max(lo, a.first[paged_block(a, s, mt)]), hi - 1);
+  }
   *t0 = lo / TK;
   *t1 = max(*t0 + 1, (hi + TK - 1) / TK);
 }
@@ -191,7 +208,7 @@ __device__ __forceinline__ int64_t paged_quot(int64_t x, int64_t y) {
 // row blocks by their lane, the others by the warp together.
 template <int M, int TK>
 __device__ __forceinline__ int64_t paged_units(const PagedLaunch& a, int b) {
-  PagedSeq s = {0, 0, 0};
+  PagedSeq s = {0, 0, 0, 0};
   if (b < a.B) s = paged_seq(a, b);
   const int prefix = b < a.B ? paged_prefix(a, b) : 0;
   const bool few = (int64_t)s.n * a.G <= 4 * M;

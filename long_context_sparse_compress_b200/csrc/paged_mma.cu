@@ -689,7 +689,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
 // measured bf16 rate.
 
 constexpr int kManyThreads = 448;  // warps 0-7 softmax (two tiles), 8-11 V, 12 copies, 13 MMA
-constexpr int kManyRows = 256;
+constexpr int kManyRows = kPagedManyRows;
 constexpr float kLazy = 8.f;       // growth of a row's maximum (base-2 units) that rescales O
 
 template <int D>
@@ -828,6 +828,20 @@ __device__ __forceinline__ void many_rescale(uint32_t o_addr, float alpha) {
     tmem_st_32(o_addr + d, o);
   }
   tmem_st_wait();
+}
+
+// The earliest document start of every block of rows, a warp per block.
+__global__ void __launch_bounds__(256) paged_first_kernel(const PagedLaunch a) {
+  grid_dep_wait();
+  const int b = blockIdx.x, lane = threadIdx.x & 31;
+  const PagedSeq s = paged_seq(a, b);
+  for (int mt = blockIdx.y * 8 + threadIdx.x / 32; (int64_t)mt * kManyRows < (int64_t)s.n * a.G; mt += gridDim.y * 8) {
+    const int i0 = paged_div(a, mt * kManyRows), i1 = paged_div(a, min(s.n * a.G, (mt + 1) * kManyRows) - 1);
+    int d = INT_MAX;
+    for (int i = i0 + lane; i <= i1; i += 32) d = min(d, a.docs[s.q0 + i]);
+    d = __reduce_min_sync(0xffffffffu, d);
+    if (lane == 0) a.first[paged_block(a, s, mt)] = d;
+  }
 }
 
 // GEN: scores are capped or biased (both forms of the loop in one kernel cost
@@ -1399,6 +1413,11 @@ cudaError_t launch_few(const PagedLaunch& a, const CUtensorMap& k, const CUtenso
 
 template <int D>
 cudaError_t launch_many(const PagedLaunch& a, const CUtensorMap& k, cudaStream_t stream) {
+  if (a.docs) {
+    const int64_t y = (a.n_tokens * a.G / kManyRows + 8) / 8;
+    const cudaError_t e = launch_pdl(paged_first_kernel, dim3(a.B, (unsigned)(y < 64 ? y : 64)), dim3(256), 0, stream, a);
+    if (e != cudaSuccess) return e;
+  }
   auto kern = a.cap > 0.f || a.slopes ? paged_many_kernel<D, true> : paged_many_kernel<D, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ManyCfg<D>::SMEM);
   if (e != cudaSuccess) return e;
