@@ -558,7 +558,7 @@ typedef struct lcsc_paged_batch {
   int64_t B, n_tokens;
   int64_t max_new;             /* >= 1: the most new tokens of one request, if known, else n_tokens; it decides
                                   the kernel's form only: no result depends on its being right */
-  int64_t max_blocks;          /* block_table row length */
+  int64_t max_blocks;          /* block_table row length; max_blocks * P <= 2^31 - 4096 */
   const int32_t* q_start;      /* [B + 1] */
   const int32_t* ctx_len;      /* [B] */
   const int32_t* block_table;  /* [B][max_blocks] */

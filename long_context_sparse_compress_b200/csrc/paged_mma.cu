@@ -670,12 +670,15 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
 // need no exchange.  O stays in TMEM; it is rescaled only when a row's maximum
 // has grown by more than 2^8 over the reference (weights then reach 256, well
 // inside f16).  V's codes become f16 numbers exactly: four warps read them
-// from global memory half a tile ahead and write code * 2^7 * (page scale /
+// from global memory a tile ahead and write code * 2^7 * (page scale /
 // largest page scale of the piece), which is exact for scales down to 2^-13 of
 // the largest and loses only what lies below 2^-31 of the largest possible |V|.
 // Two tiles keep the tensor cores busy with one while the other's weights are
 // made; a block of up to 128 rows is one tile, which the two warpgroups share by
-// taking its tiles of keys in turn and joining their O at the end.
+// taking its tiles of keys in turn and joining their O at the end (16 requests of
+// 4K to 32K tokens, 32 rows each, D = 128: 236 us, 2.4 TB/s; a million tokens for
+// 64 capped heads on one: 119 us, 2.3 TB/s; both of a CTA's chain from scores to
+// weights).
 //
 // Bound: per 256 x 128 step the products take 2,048 cycles of the tensor pipe,
 // as do the exponentials of the MUFU (32 K at 16 a cycle), and shared memory
@@ -685,7 +688,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
 // no unit holds it (no exponentials: -2%, one query term: -4%, no V
 // conversion: -8%), while larger loop bodies cost 10 to 30% and twice the
 // softmax warps 46%.  Chunk of 4096
-// tokens on 4096 cached, 64 heads on 8, D = 128: 968 us, 0.85 PFLOP/s, 52% of the
+// tokens on 4096 cached, 64 heads on 8, D = 128: 960 us, 0.86 PFLOP/s, 53% of the
 // measured bf16 rate.
 
 constexpr int kManyThreads = 448;  // warps 0-7 softmax (two tiles), 8-11 V, 12 copies, 13 MMA
@@ -1439,9 +1442,10 @@ cudaError_t launch_mma(const PagedLaunch& a, const PagedForm& f, const CUtensorM
 PagedForm paged_mma_form(int D, int G, int64_t max_new) {
   // Few rows: up to 16 per KV head and request.  From 17 on two warpgroups over
   // 128 rows are faster, however many of them are empty (16 requests of 4K to
-  // 32K tokens, 8 KV heads, D = 128, us: 8 rows 127 against 249, 16 rows 182
-  // against 252, 32 rows 307 with a few-rows kernel of that size against 258;
-  // D = 64, 32 rows: 291 against 202).
+  // 32K tokens, 8 KV heads, us: D = 128, 8 rows 121 against 230, 16 rows 160
+  // against 232, 32 rows 307 with a few-rows kernel of that size against 237;
+  // D = 64, 8 rows 108 against 179, 16 rows 157 against 180, 32 rows 291
+  // against 184).
   const int64_t rows = max_new > 16 ? 17 : max_new * G;
   if (rows > 16) return {2, kManyRows, sm_count()};
   return {1, rows <= 8 ? 8 : 16, 2 * sm_count()};

@@ -168,3 +168,9 @@ def test_python_layer_refuses_what_it_cannot_pass_on(lib):
             L.paged_attn(p, **{**good, **kw})
     with pytest.raises(L.LcscError):
         L.page_plan(16, i, i, table[:1], i, i[:1], i[:1], i, start, slots)
+
+
+def test_tables_that_end_at_the_last_position(lib):
+    """Positions are 32-bit numbers, and the kernels look some tiles ahead of the last one."""
+    b = good_batch(max_blocks=(1 << 25) - 1)
+    assert attn(lib, good_params(), b, good_pool()) == INVALID
