@@ -707,7 +707,7 @@ struct ManyCfg {
   static constexpr int OFF_V = OFF_K + 2 * kK;        // [2]
   static constexpr int OFF_P = OFF_V + 2 * kV;        // [2 tiles]
   static constexpr int OFF_BAR = OFF_P + 2 * kP;
-  static constexpr int kBars = 21;
+  static constexpr int kBars = 22;
   static constexpr int OFF_ML = OFF_BAR + (kBars + 1) / 2 * 16;  // float2 [128]: the second warpgroup's maxima and sums
   static constexpr int OFF_SCAN = OFF_ML + 128 * 8;  // PagedScratch
   static constexpr int OFF_VREF = OFF_SCAN + (int)sizeof(PagedScratch);    // int: largest V scale of the piece (bits)
@@ -864,12 +864,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   uint64_t* s_full = k_full + 8;     // [2 tiles]
   uint64_t* p_full = k_full + 10;    // [2 tiles] P is written, S is read
   uint64_t* pv_done = k_full + 12;   // [2 tiles]
-  uint64_t* q_full = k_full + 14;    // both tiles' queries
-  uint64_t* ref_full = k_full + 15;  // the piece's largest V scale
-  uint64_t* piece_done = k_full + 16;
-  uint64_t* drain = k_full + 17;
-  uint64_t* ml_full = k_full + 18;   // the second warpgroup's part of a shared block of rows
-  uint64_t* swap_full = k_full + 19;  // [2 warpgroups]
+  uint64_t* q_full = k_full + 14;    // [2 tiles] the queries
+  uint64_t* ref_full = k_full + 16;  // the piece's largest V scale
+  uint64_t* piece_done = k_full + 17;
+  uint64_t* drain = k_full + 18;
+  uint64_t* ml_full = k_full + 19;   // the second warpgroup's part of a shared block of rows
+  uint64_t* swap_full = k_full + 20;  // [2 warpgroups]
   float2* ml_s = reinterpret_cast<float2*>(sm + C::OFF_ML);
   volatile int* vref_s = reinterpret_cast<volatile int*>(sm + C::OFF_VREF);
   uint32_t* tm_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_TM);
@@ -882,9 +882,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 4), mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4), mbar_init(&pv_done[i], 1);
-      mbar_init(&swap_full[i], 4);
+      mbar_init(&swap_full[i], 4), mbar_init(&q_full[i], 4);
     }
-    mbar_init(q_full, 8);
     mbar_init(ref_full, 4);
     mbar_init(piece_done, 8);
     mbar_init(drain, 1);
@@ -944,13 +943,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const uint32_t idesc_pv = idesc_dense(0, 0, 128, D, false, true);
     const uint32_t qa = smem_u32(sm + C::OFF_Q);
     bool go = !test.stall || wait(drain, 0);  // a test of the failure path: nothing has committed to it yet
-    int n = 0, pieces = 0, cnt[2] = {0, 0};
+    int n = 0, pieces[2] = {0, 0}, cnt[2] = {0, 0};
     while (go && w.next()) {
       const PieceKeys<M, TK> keys(a, w);
       if (keys.t0 >= w.p_t1) continue;
       const bool shared = w.rows() <= 128;  // both warpgroups on one tile of rows
-      if (!(go = wait(q_full, (uint32_t)pieces & 1u))) break;
-      ++pieces;
+      if (!(go = wait(&q_full[0], (uint32_t)pieces[0]++ & 1u))) break;
+      if (!shared && !(go = wait(&q_full[1], (uint32_t)pieces[1]++ & 1u))) break;
       // Per warpgroup: Q K^T of its next tile of keys as soon as its scores are
       // read, then P V of its last one (the tile before, or, where the
       // warpgroups take the tiles in turn, the one before that).
@@ -1198,9 +1197,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           // a query that is not finite gives scores that are not numbers
           r.rf = a.sm_scale * kPagedLog2e * (amax < 0x7f80u ? pow2(ex) : NAN);
         }
+        // The second warpgroup may be a piece ahead of the first where it has no
+        // tile of keys, so it arrives for its own tile only.
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
+        if (lane == 0 && !(shared && g == 1)) mbar_arrive(&q_full[g]);
       }
       if (!(ok = wait(ref_full, (uint32_t)pieces & 1u))) break;
       ++pieces;

@@ -337,6 +337,21 @@ def test_packed_documents(cuda_lib, Hq, Hkv, D, P, cap):
     c.run(**kw).check(**kw)
 
 
+@pytest.mark.parametrize("cap", [0.0, 5.0])
+@pytest.mark.parametrize("G,D,P", [(8, 128, 64), (5, 64, 16), (20, 128, 32)])
+def test_many_short_prompts(cuda_lib, G, D, P, cap):
+    """Several short items a CTA, of one and two tiles of rows in turn, each a
+    single tile of keys; again and again with the same result."""
+    n = np.random.default_rng(G).integers(1, 41, 70)
+    c = Case(n, n, 8 * G, 8, D, P, BF16, seed=22)
+    c.run(cap=cap).check(cap=cap)
+    first, lse = c.out.clone(), c.lse.clone()
+    for _ in range(20):
+        c.run(cap=cap)
+        torch.cuda.synchronize()
+        assert torch.equal(c.out, first) and torch.equal(c.lse, lse)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("new", [[1, 1, 1, 1], [70, 5, 60, 1]])
 def test_bad_pages_lengths_and_absent_requests(cuda_lib, dtype, new):
