@@ -796,7 +796,13 @@ __device__ __forceinline__ float many_top(const PagedLaunch& a, const ManyRow& r
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(x[i]) * (i < 16 ? c0 : c1);
       if constexpr (F == kScores) {
-        if (a.cap > 0.f) many_cap(v, cap2);
+        if (a.cap > 0.f) {
+          if (!inside) {  // what lies behind the last key has no say in the cap's form
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = seen >> i & 1u ? v[i] : 0.f;
+          }
+          many_cap(v, cap2);
+        }
         if (a.slopes) many_bias(v, r, j0 + h);
       }
 #pragma unroll

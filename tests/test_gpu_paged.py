@@ -353,6 +353,25 @@ def test_many_short_prompts(cuda_lib, G, D, P, cap):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("new", [1, 3, 40])
+def test_what_ran_before_changes_no_bit(cuda_lib, dtype, new):
+    """Capped scores of lengths that end inside a tile, after calls that leave
+    small and large keys behind the last one in the shared memory."""
+    ctx = np.random.default_rng(new).integers(40, 700, 60)
+    c = Case(ctx, [new] * 60, 10, 2, 64, 16, dtype, seed=23)
+    prefix = np.random.default_rng(4).integers(0, 900, 60).astype(np.int32)
+    kw = dict(cap=5.0, prefix=prefix)
+    c.run(**kw).check(**kw)
+    first, lse = c.out.clone(), c.lse.clone()
+    other = [Case([900] * 4, [new] * 4, 10, 2, 64, 16, dtype, seed=i, spread=1 + 5 * i) for i in range(2)]
+    for i in range(20):
+        other[i % 2].run()
+        c.run(**kw)
+        torch.cuda.synchronize()
+        assert torch.equal(c.out, first) and torch.equal(c.lse, lse)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("new", [[1, 1, 1, 1], [70, 5, 60, 1]])
 def test_bad_pages_lengths_and_absent_requests(cuda_lib, dtype, new):
     """A page number outside the pool hides its tokens; ctx_len 0 takes no part;
