@@ -943,7 +943,7 @@ int32_t lcsc_paged_attn(const lcsc_paged_params* p, const lcsc_paged_batch* s, c
   if ((st = check_pool(p, cache))) return st;
   if (!s || !paged_sizes(p, s->B, s->n_tokens, s->max_new)) return LCSC_ERR_INVALID_ARG;
   // positions a few tiles past the last one are computed in 32 bits
-  if (s->max_blocks < 1 || s->max_blocks > (INT32_MAX - 4095) / p->page_size) return LCSC_ERR_INVALID_ARG;
+  if (s->max_blocks < 1 || s->max_blocks > (INT32_MAX - (kPagedAhead - 1)) / p->page_size) return LCSC_ERR_INVALID_ARG;
   if (!s->q_start || !s->ctx_len || !s->block_table) return LCSC_ERR_INVALID_ARG;
   const void* small[] = {s->q_start, s->ctx_len, s->block_table, s->lse, s->slopes, s->sink, s->prefix_len, s->doc_start};
   for (const void* q : small)

@@ -106,6 +106,10 @@ inline void paged_divisor(int d, uint32_t* mul, int* shift) {
   *mul = d == (1 << l) ? 1u << 31 : (uint32_t)(((uint64_t)1 << (31 + l)) / d + 1);
 }
 
+// A table ends this many positions before 2^31: the kernels compute positions in
+// 32 bits, some of them behind the last tile (each says how far).
+constexpr int kPagedAhead = 4096;
+
 #ifdef __CUDACC__
 
 __device__ __forceinline__ int paged_div(const PagedLaunch& a, int x) {

@@ -342,7 +342,8 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
       const PieceKeys<NR, TK> keys(a, w);
       const PageAhead<NR, TK> pages(a, w, keys);
       // lane i < per: the tile's page i
-      auto entry = [&](int t) { return pages.entry(lane < per ? t : INT_MAX, t * TK + lane * a.page); };
+      static_assert(3 * TK <= kPagedAhead, "positions of two tiles behind the last");
+      auto entry = [&](int t) { return pages.entry(lane < per ? t : INT_MAX, t * TK + (lane & (per - 1)) * a.page); };
       int32_t e1 = entry(keys.t0), e2 = entry(keys.t0 + 1);
       for (int t = keys.t0; t < keys.t1; ++t, ++n) {
         const int64_t ph = pages.place(e1);
@@ -918,7 +919,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const PieceKeys<M, TK> keys(a, w);
       const PageAhead<M, TK> pages(a, w, keys);
       // lane i < per: the tile's page i
-      auto entry = [&](int t) { return pages.entry(lane < per ? t : INT_MAX, t * TK + lane * a.page); };
+      static_assert(3 * TK <= kPagedAhead, "positions of two tiles behind the last");
+      auto entry = [&](int t) { return pages.entry(lane < per ? t : INT_MAX, t * TK + (lane & (per - 1)) * a.page); };
       int32_t e1 = entry(keys.t0), e2 = entry(keys.t0 + 1);
       for (int t = keys.t0; t < keys.t1; ++t, ++n) {
         const int64_t ph = pages.place(e1);
@@ -1026,11 +1028,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         continue;
       }
       const PageAhead<M, TK> pages(a, w, keys);
-      // the largest scale of the piece's pages
+      // the largest scale of the piece's pages, by page numbers: 128 pages on, a
+      // position may pass 2^31
       int top = 0;
-      for (int j = max(keys.t0 * TK, keys.lo / a.page * a.page) + (tid - 256) * a.page; j < min(keys.hi, w.p_t1 * TK);
-           j += 128 * a.page) {
-        const int64_t ph = pages.place(pages.entry(keys.t0, j));
+      const int last = (min(keys.hi, w.p_t1 * TK) - 1) >> a.page_log2;
+      for (int pg = (max(keys.t0 * TK, keys.lo) >> a.page_log2) + tid - 256; pg <= last; pg += 128) {
+        const int64_t ph = pages.place(pages.entry(keys.t0, pg << a.page_log2));
         if (ph >= 0) top = max(top, __float_as_int(a.v_scale[ph]));
       }
       top = __reduce_max_sync(0xffffffffu, top);
@@ -1217,6 +1220,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       // four tiles; the next four tiles' pages are looked up with these four's
       // scales, and their scales asked for a batch ahead.
       const PageAhead<M, TK> pages(a, w, keys);
+      static_assert(12 * TK <= kPagedAhead, "positions of eleven tiles behind the last");
       auto entry = [&](int t) { return pages.entry(t + lane / 8, (t + lane / 8) * TK + (lane % 8) * 16); };
       if (work) {
         const int64_t ph0 = pages.place(entry(keys.t0));
