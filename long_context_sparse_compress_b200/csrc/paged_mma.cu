@@ -150,8 +150,9 @@ struct Waits {
   volatile int* abort;
   uint32_t ns;  // of sleep between polls
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-    if (*abort) return false;
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, !*abort && mbar_try_wait(bar, parity))) return true;
+    // (one vote, as lanes apart could read the flag before and after it is set)
+    if (__any_sync(0xffffffffu, *abort)) return false;
     const bool ok = __all_sync(0xffffffffu, wait_asleep(bar, parity, ns, status, limit_ns));
     if (!ok && (threadIdx.x & 31) == 0) *abort = 1;
     return ok;
