@@ -370,9 +370,6 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
     }
     static_assert(kMaxPages <= 32, "a lane per page");
     if (lane == 0 && first) w.write_meta(true);
-    if (*abort) {  // the copies in flight land before the CTA can end
-      for (int i = n > NS ? n - NS : 0; i < n; ++i) mbar_wait(&full[i % NS], (uint32_t)(i / NS) & 1u, a.status, kDrainLimitNs);
-    }
     __syncwarp();
   } else if (warp == 5) {
     // ---------------------------------------------------------------- MMA
@@ -660,6 +657,10 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // Where a role gave up, maybe after the last copy went out, nobody may have
+  // waited for the copies in flight: they land before the CTA's memory is another's.
+  if (warp == 4 && *abort)
+    for (int i = n > NS ? n - NS : 0; i < n; ++i) mbar_wait(&full[i % NS], (uint32_t)(i / NS) & 1u, a.status, kDrainLimitNs);
   if (warp == 5) tmem_dealloc(tmem, C::kCols);
 }
 
@@ -907,12 +908,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tm_slot;  // S of tile 0, 1 (128 columns each), O of tile 0, 1
   PagedWalk<M, TK> w(a, st, share);
+  int copied = 0;  // tiles of K asked for (the copies' warp)
 
   if (warp == 12) {
     // ------------------------------------------------------------- copies
     const int per = TK >> a.page_log2;
     const uint32_t page_bytes = (uint32_t)a.page * D;
-    int n = 0;
     bool go = true, first = true;
     while (go && w.next()) {
       if (lane == 0 && first) w.write_meta(false);
@@ -923,14 +924,14 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       static_assert(3 * TK <= kPagedAhead, "positions of two tiles behind the last");
       auto entry = [&](int t) { return pages.entry(lane < per ? t : INT_MAX, t * TK + (lane & (per - 1)) * a.page); };
       int32_t e1 = entry(keys.t0), e2 = entry(keys.t0 + 1);
-      for (int t = keys.t0; t < keys.t1; ++t, ++n) {
+      for (int t = keys.t0; t < keys.t1; ++t, ++copied) {
         const int64_t ph = pages.place(e1);
         if (ph < 0 && lane < per && t * TK + lane * a.page < keys.hi && t * TK + (lane + 1) * a.page > keys.lo && a.status)
           atomicOr(a.status, LCSC_DEV_BAD_INDEX);
         e1 = e2;
         e2 = entry(t + 2);
-        const int s = n & 1;
-        if (n >= 2 && !wait(&k_empty[s], (uint32_t)((n >> 1) - 1) & 1u)) {
+        const int s = copied & 1;
+        if (copied >= 2 && !wait(&k_empty[s], (uint32_t)((copied >> 1) - 1) & 1u)) {
           go = false;
           break;
         }
@@ -943,8 +944,6 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       }
     }
     if (lane == 0 && first) w.write_meta(true);
-    if (*abort)
-      for (int i = n > 2 ? n - 2 : 0; i < n; ++i) mbar_wait(&k_full[i & 1], (uint32_t)(i >> 1) & 1u, a.status, kDrainLimitNs);
     __syncwarp();
   } else if (warp == 13) {
     // ---------------------------------------------------------------- MMA
@@ -1386,6 +1385,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // as in paged_few_kernel: copies in flight where a role gave up
+  if (warp == 12 && *abort)
+    for (int i = copied > 2 ? copied - 2 : 0; i < copied; ++i)
+      mbar_wait(&k_full[i & 1], (uint32_t)(i >> 1) & 1u, a.status, kDrainLimitNs);
   if (warp == 13) tmem_dealloc(tmem, 512);
 }
 
