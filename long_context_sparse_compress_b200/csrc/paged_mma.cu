@@ -236,9 +236,15 @@ struct PageAhead {
 // over the warps through shared memory.  Each tile's weights are taken against
 // the tile's own maxima, and its O is read back and added to the running one in
 // registers (a thread per dim), which is where rescaling happens: rows x 1
-// FMA per thread and tile instead of a read-modify-write of TMEM.  V's page
-// scales (powers of two) go into the weights, relative to the tile's
-// largest, so that weights always fill the E4M3 range.
+// FMA per thread and tile instead of a read-modify-write of TMEM.
+// V's page scales go into the weights: a key's E4M3 terms hold e^x times its
+// page's scale, from 2^8 down to steps of 2^-9.  They are taken relative to the
+// tile's largest scale, in one multiplication, where no scale of the tile is
+// below a quarter of it, and else relative to the row's own largest product of
+// weight and scale, for which the maxima are taken again with the scales'
+// exponents added.  So a row's largest product is at least 2^6, and each is off by
+// half a step of f16 (2^-11 of it) and of the third term (2^-12 of it, or 2^-10,
+// which is 2^-16 of the largest), whatever scales the tile's other pages have.
 //
 // Bound: HBM (2 D bytes per key and KV head).  Per tile the tensor pipe reads
 // 5 x 16 KB of operands (640 cycles of shared memory at D = 128 against 1,420
@@ -270,17 +276,66 @@ struct FewCfg {
   static constexpr int OFF_ROW = OFF_F2 + NR * 8;     // int4 [NR]: lo, hi, position, slope (float)
   static constexpr int OFF_QS = OFF_ROW + NR * 16;    // float [NR]: 2^e of the query row
   static constexpr int OFF_RED = OFF_QS + NR * 4;     // float [4][NR]
-  static constexpr int OFF_VMAX = OFF_RED + 4 * NR * 4;  // int [4]
-  static constexpr int OFF_M = OFF_VMAX + 16;         // float [NR]
+  static constexpr int OFF_VEND = OFF_RED + 4 * NR * 4;  // int [8]: V scales of the tile's 16-key groups, as bits
+  static constexpr int OFF_M = OFF_VEND + 32;         // float [NR]
   static constexpr int OFF_SCAN = OFF_M + NR * 4;     // PagedScratch
   static constexpr int OFF_TM = OFF_SCAN + (int)sizeof(PagedScratch);
   static constexpr int OFF_ABORT = OFF_TM + 4;
   static constexpr int SMEM = OFF_ABORT + 4 + 1024;
-  static_assert(kBars % 2 == 0 && OFF_F4 % 16 == 0 && OFF_F2 % 8 == 0 && OFF_ROW % 16 == 0 && OFF_SCAN % 8 == 0, "alignment");
+  static_assert(kBars % 2 == 0 && OFF_F4 % 16 == 0 && OFF_F2 % 8 == 0 && OFF_ROW % 16 == 0 && OFF_VEND % 16 == 0 && OFF_SCAN % 8 == 0, "alignment");
   static_assert(OFF_Q % 1024 == 0 && OFF_P % 1024 == 0 && kQBytes % 1024 == 0, "swizzle atoms");
   static_assert(kPerSm * (SMEM + 1024) <= 228 * 1024, "resident CTAs");
   static_assert(NR <= N && kPTerms * N <= PW && 3 * N <= kCols, "a key's weights, the accumulators");
 };
+
+// A key's weights as E4M3 terms: term i of row r at byte i N + r of the key's row.
+template <int NR>
+__device__ __forceinline__ void few_codes(const float (&p)[NR], uint32_t prow) {
+  constexpr int N = 16, PW = 64;
+  static_assert(FewCfg<128, NR>::N == N && FewCfg<128, NR>::PW == PW, "the weights' layout");
+  uint32_t code[kPTerms][4] = {};
+#pragma unroll
+  for (int r = 0; r < NR; r += 2) {
+    __half2 x = __floats2half2_rn(p[r], p[r + 1]);
+#pragma unroll
+    for (int term = 0; term < kPTerms; ++term) {
+      const uint32_t c8 = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(x), __NV_SATFINITE, __NV_E4M3);
+      code[term][r / 4] |= c8 << (8 * (r % 4));
+      if (term + 1 < kPTerms) x = __hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c8, __NV_E4M3)));
+    }
+  }
+#pragma unroll
+  for (int term = 0; term < kPTerms; ++term)
+    st_shared16(prow + swz<PW>(threadIdx.x, term * N), code[term][0], code[term][1], code[term][2], code[term][3]);
+}
+
+// The weights of a tile whose V scales lie far apart, in the place of those
+// that are there: scores with the exponent of the key's scale added, and weights
+// relative to the row's largest of these (a thread per key; out of line, so that
+// the loop's code stays together).
+template <int NR>
+__device__ __noinline__ void few_far(const float (&s)[NR], float vs, float m_run, float* red_s, float2* f2_s,
+                                     uint32_t prow) {
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int e = max(__float_as_int(vs) >> 23, 1) - 127;
+  const float vr = vs * pow2(-e) * 224.f;
+  float mine = -INFINITY, p[NR];
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    const float top = warp_redux_max(s[r] + (float)e);
+    if (lane == r) mine = top;
+  }
+  if (lane < NR) red_s[warp * NR + lane] = mine;
+  named_sync(1, 128);
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    const float top = fmaxf(fmaxf(red_s[r], red_s[NR + r]), fmaxf(red_s[2 * NR + r], red_s[3 * NR + r]));
+    p[r] = paged_ex2(s[r] + (float)e - (top == -INFINITY ? 0.f : top)) * vr;
+    if (tid == r) f2_s[r].y = paged_ex2(top - (m_run == -INFINITY ? 0.f : m_run)) * (1.f / 224.f);
+  }
+  few_codes<NR>(p, prow);
+  named_sync(1, 128);  // red_s is read
+}
 
 // CAP: scores are capped (the code for it, though not run, cost the plain kernel 6%).
 template <int D, int NR, bool CAP>
@@ -304,7 +359,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
   int4* row_s = reinterpret_cast<int4*>(sm + C::OFF_ROW);
   float* qs_s = reinterpret_cast<float*>(sm + C::OFF_QS);
   float* red_s = reinterpret_cast<float*>(sm + C::OFF_RED);
-  int* vmax_s = reinterpret_cast<int*>(sm + C::OFF_VMAX);
+  int* vend_s = reinterpret_cast<int*>(sm + C::OFF_VEND);
   float* m_s = reinterpret_cast<float*>(sm + C::OFF_M);
   uint32_t* tm_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_TM);
   volatile int* abort = reinterpret_cast<volatile int*>(sm + C::OFF_ABORT);
@@ -537,6 +592,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
         const bool there = ks >= 0.f && j < keys.hi;  // copied, and of this request
         const bool seen = there && j >= keys.lo;
         const float kf = ks * c2;
+        if (lane % 16 == 0) vend_s[tid / 16] = ks >= 0.f ? __float_as_int(vs) : -1;  // 16 keys lie in one page
         float s[NR];
         ok = wait(&s_full[n & 1], (uint32_t)(n >> 1) & 1u);
         if (ok) {
@@ -558,11 +614,14 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
             if (lane == r) mine = top;
           }
           if (lane < NR) red_s[warp * NR + lane] = mine;
-          const int vm = __reduce_max_sync(0xffffffffu, there ? __float_as_int(vs) : 0);
-          if (lane == 0) vmax_s[warp] = vm;
         }
         if (!(ok = named_and(1, 128, ok))) break;
-        const float vmax = __int_as_float(max(max(vmax_s[0], vmax_s[1]), max(vmax_s[2], vmax_s[3])));
+        // (bits of numbers that are not negative order as the numbers do; -1 is the
+        // least signed and the largest unsigned one)
+        const int4 va = *reinterpret_cast<const int4*>(vend_s), vb = *reinterpret_cast<const int4*>(vend_s + 4);
+        const float vmax = __int_as_float(max(max(max(max(va.x, va.y), max(va.z, va.w)), max(max(vb.x, vb.y), max(vb.z, vb.w))), 0));
+        const float vmin = __uint_as_float(min(min(min((uint32_t)va.x, (uint32_t)va.y), min((uint32_t)va.z, (uint32_t)va.w)),
+                                               min(min((uint32_t)vb.x, (uint32_t)vb.y), min((uint32_t)vb.z, (uint32_t)vb.w))));
         float al = 0.f, be = 0.f, mt = -INFINITY;
         if (tid < NR) {
           mt = fmaxf(fmaxf(red_s[tid], red_s[NR + tid]), fmaxf(red_s[2 * NR + tid], red_s[3 * NR + tid]));
@@ -579,34 +638,21 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
         // weights in [0, 256], relative to the tile's maxima and largest V scale
         const float vr = there && vmax > 0.f ? __fdividef(vs, vmax) * 256.f : 0.f;
         const uint32_t prow = smem_u32(sm + C::OFF_P);
+        float p[NR];
 #pragma unroll
-        for (int r8 = 0; r8 < N; r8 += 16) {
-          uint32_t code[kPTerms][4];
+        for (int r = 0; r < NR; r += 2) {
+          const float4 fa = f4_s[r], fb = f4_s[r + 1];
+          const float pa = paged_ex2(s[r] - fa.x), pb = paged_ex2(s[r + 1] - fb.x);
+          l[r] = fmaf(l[r], fa.y, pa * fa.z);
+          l[r + 1] = fmaf(l[r + 1], fb.y, pb * fb.z);
+          p[r] = pa * vr, p[r + 1] = pb * vr;
+        }
+        few_codes<NR>(p, prow);
+        if (vmin < 0.25f * vmax) {  // (no page at all: vmin is no number)
+          float sx[NR];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int term = 0; term < kPTerms; ++term) code[term][i] = 0;
-            if (r8 + 4 * i < NR) {
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                const int r = r8 + 4 * i + 2 * half;
-                const float4 fa = f4_s[r], fb = f4_s[r + 1];
-                const float pa = paged_ex2(s[r] - fa.x), pb = paged_ex2(s[r + 1] - fb.x);
-                l[r] = fmaf(l[r], fa.y, pa * fa.z);
-                l[r + 1] = fmaf(l[r + 1], fb.y, pb * fb.z);
-                __half2 x = __floats2half2_rn(pa * vr, pb * vr);
-#pragma unroll
-                for (int term = 0; term < kPTerms; ++term) {
-                  const uint32_t c8 = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(x), __NV_SATFINITE, __NV_E4M3);
-                  code[term][i] |= c8 << (16 * half);
-                  if (term + 1 < kPTerms) x = __hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c8, __NV_E4M3)));
-                }
-              }
-            }
-          }
-#pragma unroll
-          for (int term = 0; term < kPTerms; ++term)
-            st_shared16(prow + swz<PW>(tid, term * N + r8), code[term][0], code[term][1], code[term][2], code[term][3]);
+          for (int r = 0; r < NR; ++r) sx[r] = s[r];
+          few_far<NR>(sx, there ? vs : 0.f, m_run, red_s, f2_s, prow);
         }
         if (!there) {  // no such key: its V row may hold anything, and 0 x NaN is NaN
           uint4* v = reinterpret_cast<uint4*>(sm + C::OFF_V + (n % NS) * C::kTile + tid * D);

@@ -4,9 +4,85 @@ import pytest
 import torch
 
 from long_context_sparse_compress_b200 import lib as L
-from tests.test_gpu_paged import BF16, Case
+from oracle import formats, paged
+from tests.test_gpu_paged import BF16, F32, Case
 
 pytestmark = pytest.mark.gpu
+
+FEW, MANY = 1, 17  # hints that choose the form of few and of many rows
+
+
+def set_page(codes, scale, page, values):
+    """Values [heads][tokens][D] into a page, stored by the scale rule."""
+    s = np.vectorize(paged.scale_of)(np.abs(values).max((1, 2)))
+    scale[page] = s
+    codes[page] = formats.e4m3_encode(values / s[:, None, None])
+
+
+# ------------------------------------------------------- V scales far apart
+
+@pytest.mark.parametrize("dtype,form,ratio", [(F32, FEW, 2.0 ** -30)] + [
+    (BF16, f, 2.0 ** -r) for f, rs in ((FEW, (3, 8, 12, 20, 60)), (MANY, (8, 12, 20))) for r in rs])
+@pytest.mark.parametrize("hidden", [False, True])
+def test_pages_of_small_values_beside_large_ones(cuda_lib, dtype, form, ratio, hidden):
+    """Two pages of one tile, V of one `ratio` times the other's.  The large
+    one's keys weigh nothing (scores 2 x 22 below), or are hidden from most rows
+    by the documents while the first row sees them: the small one's values
+    come out with their own precision, not that of the neighbour's."""
+    P, D, H, n = 32, 128, 2, 5
+    c = Case([64, 64], [n, n], 2 * H, H, D, P, dtype, seed=31)
+    rng = np.random.default_rng(6)
+    small = np.array([[0, 1], [1, 0]])  # request b's small page: its second, its first
+    vsmall = 0.0
+    for b in range(2):
+        for col in range(2):
+            page, is_small = c.table[b, col], col == small[b, 1]
+            K = rng.standard_normal((H, P, D)) * 0.5
+            if not hidden:
+                K[..., 0] = 16.0 if is_small else -16.0
+            V = rng.standard_normal((H, P, D)) * (ratio if is_small else 1.0)
+            set_page(c.k, c.ks, page, K)
+            set_page(c.v, c.vs, page, V)
+            if is_small:
+                vsmall = max(vsmall, np.abs(V).max() * 1.1)
+    q = c.q.float()
+    if not hidden:
+        q[..., 0] = 16.0
+    c.q = q.to(dtype)
+    kw = {}
+    if hidden:  # request 0's rows but the first see its second page only; request 1's see everything
+        docs = np.zeros(c.N, np.int32)
+        docs[1:n] = P
+        kw["docs"] = docs
+    c.run(max_new=form, **kw)
+    torch.cuda.synchronize()
+    assert c.status.item() == 0
+    want, lse, dot, _ = paged.attention(q.to(dtype).float().numpy(), c.k, c.v, c.ks, c.vs, c.table, c.ctx, c.q_start,
+                                        np.float32(D ** -0.5), **kw)
+    rows = slice(1, n) if hidden else slice(0, 2 * n)
+    got = c.out.double().cpu().numpy()[rows]
+    want, dot = want[rows], dot[rows]
+    # score errors as in Case.check; a weight's: half a step of its 11 bits
+    # (2^-11) and of its third E4M3 term (2^-12), and what lies below the terms'
+    # last step (2^-17 of the row's largest, for each of 32 keys: 2^-12)
+    ds = (D + 8) * 2.0 ** -24 * dot / D ** 0.5 + 2.0 ** -21 * (1 + dot / D ** 0.5)
+    dp = 0.0
+    if dtype == BF16:
+        ds = ds + 2.0 ** -17 * dot / D ** 0.5
+        dp = 2.0 ** -11 + 2.0 ** -12 + 2.0 ** -12
+    tol = (2 * ds + dp + 64 * 2.0 ** -24)[..., None] * vsmall + np.abs(want) * torch.finfo(dtype).eps / 2
+    err = np.abs(got - want)
+    assert np.abs(want).max() < 2 * vsmall  # the neighbour's share is nothing
+    assert (err <= tol).all(), float((err / tol).max())
+
+
+def test_pages_of_zeros_beside_others(cuda_lib):
+    """A page of zeros has the least scale there is."""
+    for form in (FEW, MANY):
+        c = Case([190, 64], [1, 3], 4, 2, 64, 16, BF16, seed=32)
+        for page in (c.table[0, 3], c.table[0, 4], c.table[1, 0]):
+            set_page(c.v, c.vs, page, np.zeros((2, 16, 64)))
+        c.run(max_new=form).check()
 
 
 # ------------------------------------------------------------ failure path
