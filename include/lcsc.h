@@ -551,9 +551,12 @@ int32_t lcsc_paged_store(const lcsc_paged_params* p, const lcsc_paged_cache* cac
  * before or beside: every sum has a fixed order.
  * BF16 queries run on the tensor cores with float32 sums: the query is the sum
  * of E4M3 terms (values below 2^-10 of a head's largest keep an absolute
- * precision of 2^-17 of it), the softmax weights are held to 11 bits or more;
- * V components keep an absolute precision of 2^-17 or better of the largest
- * |V| that the query's pages can hold.  F32 queries run in float32 throughout. */
+ * precision of 2^-17 of it), the softmax weights are held to 11 bits.  Small
+ * weights have an absolute error: up to 16 query rows per KV head (max_new *
+ * n_heads / n_kv_heads), weight times V scale one of 2^-16 of the largest such
+ * product among the query's 128 keys around; with more, the weight one of 2^-34 of
+ * the query's largest, and V components one of 2^-32 of the largest |V| that the
+ * request's pages can hold.  F32 queries run in float32 throughout. */
 typedef struct lcsc_paged_batch {
   int64_t B, n_tokens;
   int64_t max_new;             /* >= 1: the most new tokens of one request, if known, else n_tokens; it decides

@@ -717,11 +717,12 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
 //   O [128 rows][D dims]  += P V       P and V in f16 (kind::f16)
 // A softmax warpgroup owns a tile and a thread one row of it: maxima and sums
 // need no exchange.  O stays in TMEM; it is rescaled only when a row's maximum
-// has grown by more than 2^8 over the reference (weights then reach 256, well
-// inside f16).  V's codes become f16 numbers exactly: four warps read them
+// has grown by more than 2^6.  Weights are f16 numbers from 2^15 down to steps of
+// 2^-24, the row's largest at least 2^9: 11 bits down to 2^-23 of it, and below
+// that an error of 2^-34 of it at most.  V's codes become f16 numbers exactly: four warps read them
 // from global memory a tile ahead and write code * 2^7 * (page scale /
-// largest page scale of the piece), which is exact for scales down to 2^-13 of
-// the largest and loses only what lies below 2^-31 of the largest possible |V|.
+// largest page scale of the piece), which is exact for scales down to 2^-22 of
+// the largest and loses only what lies below 2^-32 of the largest possible |V|.
 // Two tiles keep the tensor cores busy with one while the other's weights are
 // made; a block of up to 128 rows is one tile, which the two warpgroups share by
 // taking its tiles of keys in turn and joining their O at the end (16 requests of
@@ -742,7 +743,11 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
 
 constexpr int kManyThreads = 448;  // warps 0-7 softmax (two tiles), 8-11 V, 12 copies, 13 MMA
 constexpr int kManyRows = kPagedManyRows;
-constexpr float kLazy = 8.f;       // growth of a row's maximum (base-2 units) that rescales O
+// A row's weights are 2^(x - reference), the reference kDrop below the row's
+// maximum when it is taken, and taken anew, with O rescaled, when a score has
+// grown past it by more than kLazy (base-2 units): f16 weights of up to 2^15.  (Chunk of
+// 4096 tokens: 1,041 us with a drop of 9 or 7, 1,051 with 11, which rescales more.)
+constexpr float kDrop = 9.f, kLazy = 15.f;
 
 template <int D>
 struct ManyCfg {
@@ -1299,10 +1304,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           const bool fresh = t == t_first;
           float alpha = 1.f;
           bool grown = false;
-          if (top > m_ref + kLazy || (fresh && top > -INFINITY)) {
-            alpha = paged_ex2(m_ref - top);  // before the first key: 0
+          // (scores from 2^20 on are too coarse for the last part of f16's range)
+          if (top - m_ref > fmaf(fabsf(top), -0x1p-21f, kLazy) || (fresh && top > -INFINITY)) {
+            alpha = paged_ex2(m_ref - (top - kDrop));  // before the first key: 0
             grown = !fresh;
-            m_ref = top;
+            m_ref = top - kDrop;
             l *= alpha;
           }
           // P and O: the last tile's P V has read and added to them

@@ -5,7 +5,7 @@ import torch
 
 from long_context_sparse_compress_b200 import lib as L
 from oracle import formats, paged
-from tests.test_gpu_paged import BF16, F32, Case
+from tests.test_gpu_paged import BF16, F32, Case, i32, status0
 
 pytestmark = pytest.mark.gpu
 
@@ -83,6 +83,48 @@ def test_pages_of_zeros_beside_others(cuda_lib):
         for page in (c.table[0, 3], c.table[0, 4], c.table[1, 0]):
             set_page(c.v, c.vs, page, np.zeros((2, 16, 64)))
         c.run(max_new=form).check()
+
+
+# --------------------------------------------------- one key above very many
+
+@pytest.mark.parametrize("gap", [16, 18])
+@pytest.mark.parametrize("form,rows", [(FEW, 1), (MANY, 1), (MANY, 130)])
+def test_a_key_that_outweighs_very_many(cuda_lib, form, rows, gap):
+    """2^17 equal keys `gap` below two others of no value, walked by one CTA as
+    one piece (a request for each CTA, all over the same pages): what the many
+    add up to is kept."""
+    n, P, D = 1 << 17, 128, 64
+    B = torch.cuda.get_device_properties(0).multi_processor_count * (2 if form == FEW else 1)
+    k, v = (torch.zeros((n // P, 1, P, D), dtype=torch.uint8) for _ in range(2))
+    v.fill_(int(formats.e4m3_encode(np.float32(1.0))))
+    top = int(formats.e4m3_encode(np.float32(gap)))
+    assert formats.e4m3_decode(np.uint8(top)) == gap
+    for page in (0, 1):  # key 0 of the first and of the second tile
+        k[page, 0, 0, 0], v[page, 0, 0] = top, 0
+    one = torch.ones((n // P, 1))
+    cache = L.PagedCache.of(*(x.cuda() for x in (k, v, one, one)))
+    p = L.paged_params(1, 1, D, P)
+    q = torch.zeros((B * rows, 1, D), dtype=BF16)
+    q[..., 0] = 8.0  # 8 * gap / sqrt(D) = gap
+    out, lse, st = torch.zeros_like(q).cuda(), torch.zeros((B * rows, 1)).cuda(), status0()
+    table = torch.arange(n // P, dtype=torch.int32).repeat(B, 1).cuda()
+    L.paged_attn(p, q.cuda(), cache, table, i32([n] * B), i32(np.arange(B + 1) * rows), form if rows == 1 else rows, out,
+                 lse, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    others = n - rows + np.arange(rows) + 1 - 2.0  # keys that row i sees beside the two
+    den = 2 + others * np.exp(-float(gap))
+    want = others * np.exp(-float(gap)) / den
+    got = out.double().cpu().numpy().reshape(B, rows, D)
+    # a weight's half step: 2^-11 of it, or 2^-25 over 2^7 (or more) of the row's largest,
+    # for each of n keys over a sum of 2; the products' float32 sums, which add 16
+    # keys at a time (n / 16 steps of 2^-23: 2^-10) and the weights' own (a step a
+    # tile: 2^-13); the output's rounding.  Three E4M3 terms lose 2^-12 more.
+    tol = want * (2.0 ** -11 + 2.0 ** -10 + 2.0 ** -13 + 2.0 ** -9 + (2.0 ** -12 if form == FEW else 0)) + n * 2.0 ** -32 / 2
+    err = np.abs(got - want[None, :, None])
+    assert (err <= tol[None, :, None]).all(), (float(got.mean()), float(want.mean()))
+    d = np.abs(lse.double().cpu().numpy().reshape(B, rows) - float(gap) - np.log(den))
+    assert d.max() <= 2.0 ** -13
 
 
 # ------------------------------------------------------------ failure path
