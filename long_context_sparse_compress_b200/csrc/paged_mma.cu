@@ -97,6 +97,9 @@ __device__ __forceinline__ float pow2(int e) {
   return __int_as_float((e + 127) << 23);
 }
 
+// x 2^e for |e| up to 252 by two factors: 2^e itself need not be a number, or a normal one.
+__device__ __forceinline__ float times_pow2(float x, int e) { return x * pow2(e / 2) * pow2(e - e / 2); }
+
 __device__ __forceinline__ float warp_redux_max(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
@@ -533,11 +536,10 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
           for (int i = 0; i < VPL; ++i) amax = fmaxf(amax, fabsf(v[i]));
           amax = warp_max(amax);
           const int ex = amax > 0.f ? (int)(__float_as_uint(amax) >> 23) - 127 - 7 : 0;
-          const float f = pow2(-ex);
           uint16_t hi[VPL / 2], lo[VPL / 2];
 #pragma unroll
           for (int i = 0; i < VPL / 2; ++i) {
-            const float x = v[2 * i] * f, y = v[2 * i + 1] * f;
+            const float x = times_pow2(v[2 * i], -ex), y = times_pow2(v[2 * i + 1], -ex);
             hi[i] = e4m3x2_code(x, y);
             const float2 h = e4m3x2_val(hi[i]);
             lo[i] = e4m3x2_code(x - h.x, y - h.y);
@@ -551,7 +553,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
             *reinterpret_cast<uint16_t*>(q + C::kQBytes) = lo[0];
           }
           // a query that is not finite gives scores that are not numbers
-          if (lane == 0 && r < NR) qs_s[r] = amax <= 3.402823466e38f ? pow2(ex) : NAN;
+          if (lane == 0 && r < NR) qs_s[r] = amax <= 3.402823466e38f ? times_pow2(1.f, ex) : NAN;
         }
         fence_async_smem();
         __syncwarp();
@@ -775,7 +777,7 @@ struct ManyCfg {
 // One row's scores: factors, mask and bias of the thread's query row.
 struct ManyRow {
   int lo, hi, pos;
-  float rf, slope;  // sm_scale log2(e) 2^e of the query; bias per position in base-2 units
+  float rf, slope;  // 2^e of the query; bias per position in base-2 units
 };
 
 // Bits of the keys j .. j + 31 that the row sees; `there`: bit i for a page of the keys j + 16 i ..
@@ -822,7 +824,7 @@ __device__ __forceinline__ void many_bias(float (&v)[32], const ManyRow& r, int 
 }
 
 // A row's largest score over the keys h0 .. h1 of a tile, in base-2 units; lanes of .. of + 7 of
-// `ks` hold the K scales of the tile's 16-key groups (-1: not there).  Three forms:
+// `ks` hold the factors of the tile's 16-key groups (below 0: not there).  Three forms:
 //   kPlain:  every row of the warp sees every key, no cap, no bias: the largest
 //            raw product of each page, times its factor
 //   kMasked: no cap, no bias
@@ -1166,7 +1168,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     // ------------------------------------------------------------ softmax
     const int g = warp / 4;  // the tile
     const int row_in = tid % 128;
-    const float cap2 = a.cap * kPagedLog2e;
+    const float c2 = a.sm_scale * kPagedLog2e, cap2 = a.cap * kPagedLog2e;
     const uint32_t lane_base = (uint32_t)((warp % 4) * 32) << 16;
     const uint32_t s_addr = tmem + g * 128 + lane_base, o_addr = tmem + 256 + g * 128 + lane_base;
     bool ok = true;
@@ -1237,12 +1239,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
               const uint32_t own = __shfl_sync(0xffffffffu, top, lane % RPI * LPR);
               if (lane / RPI == i0 + i) amax = own;
               if (shared && g == 1) continue;  // the first warpgroup lays them out
-              const float f = pow2(top ? 134 - (int)(top >> 7) : 0);
+              const int up = top ? 134 - (int)(top >> 7) : 0;
               const uint32_t wd[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
               uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                const float y0 = __uint_as_float(wd[q] << 16) * f, y1 = __uint_as_float(wd[q] & 0xffff0000u) * f;
+                const float y0 = times_pow2(__uint_as_float(wd[q] << 16), up),
+                            y1 = times_pow2(__uint_as_float(wd[q] & 0xffff0000u), up);
                 const uint16_t hc = e4m3x2_code(y0, y1);
                 const float2 h = e4m3x2_val(hc);
                 hi[q / 2] |= (uint32_t)hc << (16 * (q & 1));
@@ -1255,7 +1258,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           }
           const int ex = amax ? (int)(amax >> 7) - 134 : 0;
           // a query that is not finite gives scores that are not numbers
-          r.rf = a.sm_scale * kPagedLog2e * (amax < 0x7f80u ? pow2(ex) : NAN);
+          r.rf = amax < 0x7f80u ? times_pow2(1.f, ex) : NAN;
         }
         // The second warpgroup may be a piece ahead of the first where it has no
         // tile of keys, so it arrives for its own tile only.
@@ -1267,8 +1270,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       ++pieces;
       const float vref = __int_as_float(*vref_s);
       float m_ref = -INFINITY, l = 0.f;
-      // Lane i holds the K scale of the keys 16 (i % 8) .. of the i / 8th of
-      // four tiles; the next four tiles' pages are looked up with these four's
+      // Lane i holds the K scale (times the softmax's) of the keys 16 (i % 8) .. of
+      // the i / 8th of four tiles; the next four tiles' pages are looked up with these four's
       // scales, and their scales asked for a batch ahead.
       const PageAhead<M, TK> pages(a, w, keys);
       static_assert(12 * TK <= kPagedAhead, "positions of eleven tiles behind the last");
@@ -1282,7 +1285,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         for (int t = t_first; t < keys.t1; t += t_step) {
           const int of4 = (t - keys.t0) & 3;
           if (of4 < t_step) {  // the first of four tiles, or of this warpgroup's two of them
-            ks = ks_next;
+            ks = ks_next * c2;
             const int64_t ph1 = pages.place(e1);
             ks_next = ld_if(a.k_scale + ph1, ph1 >= 0, -1.f);
             e1 = entry(t - of4 + 8);

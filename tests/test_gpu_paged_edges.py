@@ -127,6 +127,19 @@ def test_a_key_that_outweighs_very_many(cuda_lib, form, rows, gap):
     assert d.max() <= 2.0 ** -13
 
 
+# --------------------------------------------- queries near the least magnitude
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("new,form", [([1, 3], FEW), ([1, 3], MANY), ([60, 30], 60)])
+def test_queries_near_the_least_magnitude(cuda_lib, dtype, new, form):
+    """Queries down to subnormal numbers against keys near the largest."""
+    c = Case([150, 40], new, 8, 2, 64, 16, dtype, seed=33)
+    small = 2.0 ** -np.array([119, 121, 123, 124, 125, 126, 128, 130.0])
+    c.q = (c.q.float() * torch.from_numpy(small).float()[None, :, None]).to(dtype)
+    c.ks *= np.float32(2.0 ** 120)
+    c.run(max_new=form).check()
+
+
 # ------------------------------------------------------------ failure path
 
 @pytest.mark.parametrize("stall", [True, False])
