@@ -272,15 +272,18 @@ def _ws_size(fn, *args):
     return out.value
 
 
-def workspace(nbytes, device="cuda"):
-    return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
+def workspace(nbytes, device="cuda", stream=None):
+    """Device memory for a call.  It belongs to the call's stream: once dropped,
+    it may serve what comes later on that stream, even while the call runs."""
+    with torch.cuda.stream(stream):  # (None: the current one)
+        return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
 
 
 def compress(p, tensor, x, B, tok_begin, tok_end, w, bpos, entries, window=None, status=None,
              hca=False, stream=None):
     lib = load()
     n_tok = tok_end - tok_begin
-    ws = workspace(_ws_size(lib.lcsc_compress_workspace_size, ctypes.byref(p), B, n_tok), x.device)
+    ws = workspace(_ws_size(lib.lcsc_compress_workspace_size, ctypes.byref(p), B, n_tok), x.device, stream)
     fn = lib.lcsc_hca_compress if hca else lib.lcsc_csa_compress
     win = window.c() if window is not None else None
     check(fn(ctypes.byref(p), TENSOR[tensor], ptr(x), B, tok_begin, tok_end, ptr(w), ptr(bpos),
@@ -304,7 +307,7 @@ def index_topk(p, q_idx, w_idx, keys, ctx_len, n_max, out_idx, out_score=None, w
     lib = load()
     B, T = q_idx.shape[0], q_idx.shape[1]
     if ws is None:
-        ws = workspace(index_topk_workspace(p, B, T, n_max), q_idx.device)
+        ws = workspace(index_topk_workspace(p, B, T, n_max), q_idx.device, stream)
     check(lib.lcsc_csa_index_topk(ctypes.byref(p), ptr(q_idx), ptr(w_idx), ctypes.byref(keys.c()),
                                   ptr(ctx_len), B, T, n_max, ptr(out_idx), ptr(out_score), ptr(ws),
                                   ws.numel(), ptr(status), stream_handle(stream)))
@@ -338,7 +341,7 @@ def sparse_attn(p, q, kv, v, win_kv, win_v, idx, sink, ctx_len, out, lse=None, w
     lib = load()
     B, T = q.shape[0], q.shape[1]
     if ws is None:
-        ws = workspace(attn_workspace(p, B, T, kv.capacity, False), q.device)
+        ws = workspace(attn_workspace(p, B, T, kv.capacity, False), q.device, stream)
     check(lib.lcsc_csa_sparse_attn(
         ctypes.byref(p), ptr(q), ctypes.byref(kv.c()), _cref(v), ctypes.byref(win_kv.c()), _cref(win_v),
         ptr(idx), ptr(sink), _cref(sink_kv), _cref(sink_v), ptr(ctx_len), B, T, ptr(out), ptr(lse), ptr(ws),
@@ -351,7 +354,7 @@ def dense_attn(p, q, kv, v, win_kv, win_v, sink, ctx_len, n_max, out, lse=None, 
     lib = load()
     B, T = q.shape[0], q.shape[1]
     if ws is None:
-        ws = workspace(attn_workspace(p, B, T, n_max, True), q.device)
+        ws = workspace(attn_workspace(p, B, T, n_max, True), q.device, stream)
     check(lib.lcsc_hca_dense_attn(
         ctypes.byref(p), ptr(q), ctypes.byref(kv.c()), _cref(v), ctypes.byref(win_kv.c()), _cref(win_v),
         ptr(sink), _cref(sink_kv), _cref(sink_v), ptr(ctx_len), B, T, n_max, ptr(out), ptr(lse), ptr(ws),
@@ -531,7 +534,7 @@ def page_plan(page_size, cached, n_new, block_table, free_pages, n_free, n_free_
     st, handle = arg.dense("status", status, _I32), None
     if ws is None:
         handle = arg.handle()
-        ws = workspace(page_plan_workspace(B), cached.device)
+        ws = workspace(page_plan_workspace(B), cached.device, stream)
     wp = arg.dense("ws", ws, torch.uint8)
     check(load().lcsc_page_plan(page_size, B, n, block_table.shape[1], free_pages.numel(), *ints, wp, ws.numel(), st,
                                 handle or arg.handle()))
@@ -574,7 +577,7 @@ def paged_attn(p, q, cache, block_table, ctx_len, q_start, max_new, out, lse=Non
     st, handle = dense("status", status, _I32), None
     if ws is None:
         handle = arg.handle()
-        ws = workspace(paged_attn_workspace(p, B, n, max_new), q.device)
+        ws = workspace(paged_attn_workspace(p, B, n, max_new), q.device, stream)
     wp = dense("ws", ws, torch.uint8)
     check(load().lcsc_paged_attn(ctypes.byref(p), ctypes.byref(batch), ctypes.byref(pool), wp, ws.numel(), st,
                                  handle or arg.handle()))

@@ -140,6 +140,29 @@ def test_queries_near_the_least_magnitude(cuda_lib, dtype, new, form):
     c.run(max_new=form).check()
 
 
+# -------------------------------------------------------------- workspaces
+
+def test_a_workspace_of_the_call_belongs_to_its_stream(cuda_lib):
+    """Memory that a call takes for itself is not given to another stream while
+    the call may still run."""
+    c = Case([400, 300], [3, 1], 8, 2, 64, 16, BF16, seed=37).run()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    ints = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")
+    plan = (16, i32([5, 0]), i32([1, 3]), i32([[0, -1], [-1, -1]]), i32([1, 2, 3]), i32([3]), ints(1), ints(2), ints(3),
+            ints(4))
+    torch.cuda.synchronize()
+    for call in (lambda: L.paged_attn(*c.pos, **{**c.args, "ws": None, "stream": s}),
+                 lambda: L.page_plan(*plan, stream=s)):
+        ws = call()
+        at, n = ws.data_ptr(), ws.numel()
+        del ws
+        again = [L.workspace(n) for _ in range(4)]
+        assert at not in [x.data_ptr() for x in again]
+        s.synchronize()
+    c.check()
+
+
 # ------------------------------------------------------------ failure path
 
 @pytest.mark.parametrize("stall", [True, False])
