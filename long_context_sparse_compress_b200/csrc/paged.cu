@@ -512,6 +512,11 @@ __global__ void __launch_bounds__(kFmaThreads) paged_fma_kernel(const __grid_con
     int item_lo, item_hi, x;
     paged_span(a, w.p_s, paged_prefix(a, w.p_b), paged_div(a, r0), &item_lo, &x);
     paged_span(a, w.p_s, paged_prefix(a, w.p_b), paged_div(a, r0 + rows - 1), &x, &item_hi);
+    if (a.docs && w.p_s.L > 0) {  // pages before every row's document are not looked at
+      int first_doc = INT_MAX;
+      for (int i = paged_div(a, r0); i <= paged_div(a, r0 + rows - 1); ++i) first_doc = min(first_doc, a.docs[w.p_s.q0 + i]);
+      item_lo = max(item_lo, first_doc);
+    }
     const int32_t* table = a.table + (int64_t)w.p_b * a.max_blocks;
     __syncthreads();  // the last piece is done with shared memory
     if (tid < M) {

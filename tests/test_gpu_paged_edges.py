@@ -140,6 +140,20 @@ def test_queries_near_the_least_magnitude(cuda_lib, dtype, new, form):
     c.run(max_new=form).check()
 
 
+# ------------------------------------------------- what no query of a step sees
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("new", [[1, 4], [40, 30]])
+def test_documents_pass_over_released_pages(cuda_lib, dtype, new):
+    """Pages before every row's document may be gone from the table."""
+    c = Case([300, 500], new, 8, 2, 128, 16, dtype, seed=34)
+    docs = np.repeat([150, 333], new).astype(np.int32)
+    docs = np.concatenate([docs, np.zeros(c.N - len(docs), np.int32)])
+    table = c.table.copy()
+    table[0, :150 // 16], table[1, :333 // 16] = -1, c.n_pages + 5
+    c.run(table=table, docs=docs).check(docs=docs)
+
+
 # -------------------------------------------------------------- workspaces
 
 def test_a_workspace_of_the_call_belongs_to_its_stream(cuda_lib):
