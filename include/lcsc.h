@@ -543,8 +543,9 @@ int32_t lcsc_paged_store(const lcsc_paged_params* p, const lcsc_paged_cache* cac
  * zeros and -inf (LCSC_DEV_BAD_LENGTH); rows of a q_start that falls or passes
  * n_tokens are not written (LCSC_DEV_BAD_LENGTH).  A page number outside the
  * pool hides its tokens (LCSC_DEV_BAD_INDEX); pages that no query of the step
- * sees are not looked at.  Codes of visible tokens are never 0x7F or 0xFF (the
- * store writes none); rows of a page past the request's end may hold anything.
+ * sees are not looked at.  From the first token that a query of the step sees to
+ * the request's last, codes are never 0x7F or 0xFF (the store writes none); the
+ * rows of a page before and behind them may hold anything.
  * The workspace (lcsc_paged_attn_workspace_size() bytes, the same for every
  * length) serves one call at a time: calls that may overlap, replays of
  * captured ones among them, need one each.  Results do not depend on what ran

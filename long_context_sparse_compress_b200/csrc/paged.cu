@@ -539,8 +539,8 @@ __global__ void __launch_bounds__(kFmaThreads) paged_fma_kernel(const __grid_con
       }
       q_s[r][d] = v;
     }
-    auto page_of = [&](int key) -> int64_t {  // (page, head) index of a key's page, or -1
-      if (key >= item_hi || (key | (a.page - 1)) < item_lo) return -1;
+    auto page_of = [&](int key) -> int64_t {  // (page, head) index of a key's page, or -1 (no row sees the key)
+      if (key >= item_hi || key < item_lo) return -1;
       const int32_t pg = table[key >> a.page_log2];
       if (pg < 0 || pg >= a.n_pages) {
         if (a.status) atomicOr(a.status, LCSC_DEV_BAD_INDEX);

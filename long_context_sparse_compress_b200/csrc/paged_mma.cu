@@ -591,8 +591,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
         const float ks_next = ld_if(a.k_scale + ph1, ph1 >= 0, -1.f), vs_next = ld_if(a.v_scale + ph1, ph1 >= 0, 0.f);
         e1 = pages.entry(t + 2, (t + 2) * TK + tid);
         const int j = t * TK + tid;
-        const bool there = ks >= 0.f && j < keys.hi;  // copied, and of this request
-        const bool seen = there && j >= keys.lo;
+        const bool there = ks >= 0.f && j >= keys.lo && j < keys.hi;  // copied, and seen by some row
         const float kf = ks * c2;
         if (lane % 16 == 0) vend_s[tid / 16] = ks >= 0.f ? __float_as_int(vs) : -1;  // 16 keys lie in one page
         float s[NR];
@@ -609,7 +608,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
             float y = __uint_as_float(x[r]) * (kf * qs_s[r]);
             if constexpr (CAP) y = paged_cap(y, cap2);
             if (a.slopes) y -= __int_as_float(row_s[r].w) * (float)abs(row_s[r].z - j);
-            bool see = seen;
+            bool see = there;
             if (!inside) see = see && j >= row_s[r].x && j < row_s[r].y;
             s[r] = see ? y : -INFINITY;
             const float top = warp_redux_max(s[r]);
@@ -656,7 +655,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
           for (int r = 0; r < NR; ++r) sx[r] = s[r];
           few_far<NR>(sx, there ? vs : 0.f, m_run, red_s, f2_s, prow);
         }
-        if (!there) {  // no such key: its V row may hold anything, and 0 x NaN is NaN
+        if (!there) {  // no row sees the key: its V may hold anything, and 0 x NaN is NaN
           uint4* v = reinterpret_cast<uint4*>(sm + C::OFF_V + (n % NS) * C::kTile + tid * D);
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) v[i] = make_uint4(0, 0, 0, 0);
@@ -1114,9 +1113,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         const int64_t ph = pages.place(e[half]);
         sc[half] = ld_if(a.v_scale + ph, ph >= 0, 0.f);
         const int j0 = key + rsub;
+        const uint32_t span = (uint32_t)(keys.hi - keys.lo);
         const uint8_t* src = a.v + (ph * a.page + (j0 & (a.page - 1))) * D + c * 16;
 #pragma unroll
-        for (int i = 0; i < HI; ++i) raw[half][i] = ld_if(src + i * RPI * D, ph >= 0 && j0 + i * RPI < keys.hi);
+        for (int i = 0; i < HI; ++i)  // zeros for the keys that no row sees
+          raw[half][i] = ld_if(src + i * RPI * D, ph >= 0 && (uint32_t)(j0 + i * RPI - keys.lo) < span);
       };
 #pragma unroll
       for (int half = 0; half < 2; ++half) {

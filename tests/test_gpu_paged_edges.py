@@ -154,6 +154,24 @@ def test_documents_pass_over_released_pages(cuda_lib, dtype, new):
     c.run(table=table, docs=docs).check(docs=docs)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("new", [[1, 4], [40, 30]])
+@pytest.mark.parametrize("mask", ["window", "docs"])
+def test_rows_of_a_page_before_the_first_visible_may_hold_anything(cuda_lib, dtype, new, mask):
+    c = Case([300, 500], new, 8, 2, 128, 64, dtype, seed=35)
+    if mask == "window":
+        kw, first = dict(window=40), [max(0, t - n + 1 - 40) for t, n in zip(c.ctx, new)]
+    else:
+        first = [150, 333]
+        docs = np.repeat(first, new).astype(np.int32)
+        kw = dict(docs=np.concatenate([docs, np.zeros(c.N - len(docs), np.int32)]))
+    for b, lo in enumerate(first):
+        assert lo % 64
+        for codes in (c.k, c.v):
+            codes[c.table[b, lo // 64], :, :lo % 64] = 0x7F
+    c.run(**kw).check(**kw)
+
+
 # -------------------------------------------------------------- workspaces
 
 def test_a_workspace_of_the_call_belongs_to_its_stream(cuda_lib):
