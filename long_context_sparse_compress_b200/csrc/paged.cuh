@@ -456,16 +456,19 @@ __device__ __forceinline__ float paged_close(const PagedLaunch& a, const PagedSe
                                              float l, bool write_lse, int64_t* at) {
   const int i = paged_div(a, row), head = h * a.G + row - i * a.G;
   *at = (s.q0 + i) * a.Hq + head;
-  float f = 1.f;
+  float f = 1.f, top_e = top * kPagedLn2;
   if (a.sink && s.L > 0) {
-    const float sg = a.sink[head] * kPagedLog2e, m = fmaxf(top, sg);
+    const float sink = a.sink[head];
+    float sg = sink * kPagedLog2e;  // finite where the sink is: the type's largest numbers pass it here
+    if (fabsf(sg) > 3.402823466e38f && sink != -INFINITY) sg = copysignf(3.402823466e38f, sg);
+    const float m = fmaxf(top, sg);
     if (m != -INFINITY) {
       f = paged_ex2(top - m);  // top -inf: 0
       l = fmaf(l, f, paged_ex2(sg - m));
-      top = m;
+      if (sg >= top) top_e = sink;
     }
   }
-  if (write_lse && a.lse) a.lse[*at] = l == 0.f ? -INFINITY : (top + log2f(l)) * kPagedLn2;
+  if (write_lse && a.lse) a.lse[*at] = l == 0.f ? -INFINITY : fmaf(log2f(l), kPagedLn2, top_e);
   return l == 0.f ? 0.f : f / l;  // a sum that is no number stays one
 }
 

@@ -172,6 +172,21 @@ def test_rows_of_a_page_before_the_first_visible_may_hold_anything(cuda_lib, dty
     c.run(**kw).check(**kw)
 
 
+# ------------------------------------------------------------------- sinks
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("new", [[1, 1, 1], [40, 3, 30]])
+def test_sinks_of_any_size(cuda_lib, dtype, new):
+    """The largest and least values of the type, and none (minus infinity), of
+    rows that see something and of rows that see nothing."""
+    big = float(np.finfo(np.float32).max)
+    c = Case([3000, 40, 64], new, 8, 2, 64, 16, dtype, seed=36)
+    docs = np.zeros(c.N, np.int32)
+    docs[c.q_start[1]:c.q_start[2]] = 1 << 30
+    kw = dict(sink=np.array([big, -big, -np.inf, 2.5e38, 3e38, -3e38, 80.0, 0.0], np.float32), docs=docs)
+    c.run(**kw).check(**kw)
+
+
 # -------------------------------------------------------------- workspaces
 
 def test_a_workspace_of_the_call_belongs_to_its_stream(cuda_lib):
