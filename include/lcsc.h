@@ -501,7 +501,8 @@ typedef struct lcsc_paged_cache {
  * either), or when its length is negative or passes max_blocks * P or its rows
  * pass n_tokens (LCSC_DEV_BAD_LENGTH).  Rows from q_start[B] on get slot and
  * position -1.  A stack that would grow past n_pages drops the pages above
- * (LCSC_DEV_BAD_INDEX).  workspace: lcsc_page_plan_workspace_size() bytes. */
+ * (LCSC_DEV_BAD_INDEX).  But for n_free_out, no output may overlap another array
+ * of the call.  workspace: lcsc_page_plan_workspace_size() bytes. */
 int32_t lcsc_page_plan_workspace_size(int64_t B, size_t* bytes);
 int32_t lcsc_page_plan(int32_t page_size, int64_t B, int64_t n_tokens, int64_t max_blocks, int64_t n_pages,
                        const int32_t* cached, const int32_t* n_new, int32_t* block_table,

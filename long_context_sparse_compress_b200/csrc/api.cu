@@ -868,6 +868,15 @@ int32_t lcsc_page_plan(int32_t page_size, int64_t B, int64_t n_tokens, int64_t m
   for (const void* q : all)
     if (!aligned4(q)) return LCSC_ERR_INVALID_ARG;
   if (!workspace || !aligned16(workspace) || workspace_bytes < need) return LCSC_ERR_WORKSPACE;
+  // The rows are filled in from the inputs once the lengths are written: an output
+  // in an input's place would lead to pages that nobody has.
+  const int64_t sizes[] = {B, B, B * max_blocks, n_pages, 1, 1, B, B + 1, n_tokens, positions ? n_tokens : 0};
+  for (int i = 0; i < 10; ++i)
+    for (int j = 0; j < i; ++j) {
+      const bool inputs = j < 2 && (i < 2 || i == 4), height = i == 5 && j == 4 && all[i] == all[j];
+      const int32_t *x = (const int32_t*)all[i], *y = (const int32_t*)all[j];
+      if (!inputs && !height && x < y + sizes[j] && y < x + sizes[i]) return LCSC_ERR_INVALID_ARG;
+    }
   PagePlanLaunch L;
   L.page = page_size;
   L.page_log2 = log2_of(page_size);

@@ -1,4 +1,6 @@
 """Limits of the paged calls' arguments, on the host before any launch (CPU only)."""
+import ctypes
+
 import pytest
 
 from tests.test_paged_args import INVALID, WORKSPACE, attn, good_batch, good_params, good_pool, lib  # noqa: F401
@@ -13,3 +15,25 @@ def test_longest_table(lib, page):  # noqa: F811
     p = good_params(page_size=page)
     assert attn(lib, p, good_batch(max_blocks=most), good_pool(), None) == WORKSPACE
     assert attn(lib, p, good_batch(max_blocks=most + 1), good_pool(), None) == INVALID
+
+
+def test_plan_refuses_outputs_in_the_place_of_other_arrays(lib):  # noqa: F811
+    """Lengths written over their inputs, say, or over an array's last number."""
+    out = ctypes.c_size_t(0)
+    assert lib.lcsc_page_plan_workspace_size(3, ctypes.byref(out)) == 0
+    names = ("cached", "n_new", "table", "free", "n_free", "left", "ctx", "q_start", "slots", "pos")
+    sizes = dict(cached=3, n_new=3, table=12, free=10, n_free=1, left=1, ctx=3, q_start=4, slots=5, pos=5)
+    at, apart = 1 << 16, {}
+    for name in names:
+        apart[name], at = at, at + 4 * sizes[name]  # one right behind the other
+
+    def call(**kw):
+        a = {**apart, **kw}
+        return lib.lcsc_page_plan(64, 3, 5, 4, 10, *(a[n] for n in names), 256, out.value, None, None)
+
+    for i, a in enumerate(names):
+        for b in names[:i]:
+            if (a, b) in (("n_new", "cached"), ("n_free", "cached"), ("n_free", "n_new"), ("left", "n_free")):
+                continue
+            for shift in {0, 4 * (sizes[b] - 1)}:  # the same place, and the other's last number
+                assert call(**{a: apart[b] + shift}) == INVALID, (a, b, shift)
