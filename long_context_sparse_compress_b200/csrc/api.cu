@@ -864,7 +864,7 @@ int32_t lcsc_page_plan(int32_t page_size, int64_t B, int64_t n_tokens, int64_t m
   if (!cached || !n_new || !block_table || !free_pages || !n_free || !n_free_out || !ctx_len || !q_start)
     return LCSC_ERR_INVALID_ARG;
   if (n_tokens > 0 && !slots) return LCSC_ERR_INVALID_ARG;
-  const void* all[] = {cached, n_new, block_table, free_pages, n_free, n_free_out, ctx_len, q_start, slots, positions};
+  const void* all[] = {cached, n_new, block_table, free_pages, n_free, n_free_out, ctx_len, q_start, slots, positions, status};
   for (const void* q : all)
     if (!aligned4(q)) return LCSC_ERR_INVALID_ARG;
   if (!workspace || !aligned16(workspace) || workspace_bytes < need) return LCSC_ERR_WORKSPACE;
@@ -911,7 +911,7 @@ int32_t lcsc_paged_store(const lcsc_paged_params* p, const lcsc_paged_cache* cac
   const int64_t values = (int64_t)p->n_kv_heads * p->head_dim;
   if ((st = check_rows(k, k_stride, values, p->x_dtype))) return st;
   if ((st = check_rows(v, v_stride, values, p->x_dtype))) return st;
-  if (!slots || !aligned4(slots)) return LCSC_ERR_INVALID_ARG;
+  if (!slots || !aligned4(slots) || !aligned4(status)) return LCSC_ERR_INVALID_ARG;
   PagedStoreLaunch L;
   L.codes[0] = reinterpret_cast<uint8_t*>(cache->k);
   L.codes[1] = reinterpret_cast<uint8_t*>(cache->v);
@@ -954,7 +954,7 @@ int32_t lcsc_paged_attn(const lcsc_paged_params* p, const lcsc_paged_batch* s, c
   // positions a few tiles past the last one are computed in 32 bits
   if (s->max_blocks < 1 || s->max_blocks > (INT32_MAX - (kPagedAhead - 1)) / p->page_size) return LCSC_ERR_INVALID_ARG;
   if (!s->q_start || !s->ctx_len || !s->block_table) return LCSC_ERR_INVALID_ARG;
-  const void* small[] = {s->q_start, s->ctx_len, s->block_table, s->lse, s->slopes, s->sink, s->prefix_len, s->doc_start};
+  const void* small[] = {s->q_start, s->ctx_len, s->block_table, s->lse, s->slopes, s->sink, s->prefix_len, s->doc_start, status};
   for (const void* q : small)
     if (!aligned4(q)) return LCSC_ERR_INVALID_ARG;
   if (s->n_tokens == 0) return LCSC_OK;

@@ -37,3 +37,14 @@ def test_plan_refuses_outputs_in_the_place_of_other_arrays(lib):  # noqa: F811
                 continue
             for shift in {0, 4 * (sizes[b] - 1)}:  # the same place, and the other's last number
                 assert call(**{a: apart[b] + shift}) == INVALID, (a, b, shift)
+
+
+def test_status_words_of_no_alignment(lib):  # noqa: F811
+    """A device atomic on such an address would be a fault."""
+    p, c, b = good_params(), good_pool(), good_batch()
+    out = ctypes.c_size_t(0)
+    assert lib.lcsc_page_plan_workspace_size(3, ctypes.byref(out)) == 0
+    for status in (1, 2, 4098):
+        assert lib.lcsc_paged_attn(ctypes.byref(p), ctypes.byref(b), ctypes.byref(c), 4096, 1 << 40, status, None) == INVALID
+        assert lib.lcsc_paged_store(ctypes.byref(p), ctypes.byref(c), 16, 256, 32, 256, 16, 1, status, None) == INVALID
+        assert lib.lcsc_page_plan(64, 3, 5, 4, 10, *(1 << k for k in range(10, 20)), 256, out.value, status, None) == INVALID
