@@ -163,7 +163,7 @@ struct Waits {
 };
 
 // First and past the last position that any row of a piece sees (a whole warp
-// computes it), and the first tile of the piece that holds one.
+// computes it), and the first tile of the piece that holds one (t1: none does).
 template <int M, int TK>
 struct PieceKeys {
   int lo, hi, t0, t1;
@@ -179,7 +179,7 @@ struct PieceKeys {
       lo = max(lo, __reduce_min_sync(0xffffffffu, d));
     }
     t1 = w.p_t1;
-    t0 = min(t1, max(w.p_t0, lo / TK));
+    t0 = lo < hi ? min(t1, max(w.p_t0, lo / TK)) : t1;
   }
 };
 

@@ -172,6 +172,20 @@ def test_rows_of_a_page_before_the_first_visible_may_hold_anything(cuda_lib, dty
     c.run(**kw).check(**kw)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("new", [[1, 4, 2], [40, 30, 2]])
+@pytest.mark.parametrize("behind", [0, 5, 1 << 30])
+def test_requests_whose_documents_begin_behind_the_last_token(cuda_lib, dtype, new, behind):
+    """They see nothing, also where what lies behind the last token is in its tile and page."""
+    c = Case([300, 500, 100], new, 8, 2, 128, 128, dtype, seed=38)
+    docs = np.zeros(c.N, np.int32)
+    docs[:new[0]] = 300 + behind
+    docs[new[0] + new[1]:] = 100 + behind
+    kw = dict(docs=docs, sink=np.linspace(-3, 3, 8).astype(np.float32))
+    c.run(**kw).check(**kw)
+    c.run(docs=docs).check(docs=docs)
+
+
 # ------------------------------------------------------------------- sinks
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
