@@ -60,7 +60,7 @@
 extern "C" {
 #endif
 
-#define LCSC_ABI_VERSION 4
+#define LCSC_ABI_VERSION 5
 
 /* Return codes. */
 #define LCSC_OK 0
@@ -533,10 +533,13 @@ int32_t lcsc_paged_store(const lcsc_paged_params* p, const lcsc_paged_cache* cac
 /* Attention of the new tokens over the cached ones (their own K and V among
  * them).  The query of token i of request b, head h, sits at position
  * p = ctx_len[b] - (q_start[b + 1] - q_start[b]) + i and sees the positions
- *   max(0, p - window + 1, doc_start[row]) <= j < min(ctx_len[b], max(p + 1, prefix_len[b])),
- * with
+ *   max(0, p - window + 1, doc_start[row]) <= j < min(ctx_len[b], max(p + 1, prefix_len[b]), doc_end[row])
+ * (each bound where it is given), with
  *   x_j = sm_scale q . K_j;   x_j = c tanh(x_j / c) if softcap;   x_j -= slopes[h] |p - j|;
  *   out = sum_j e^{x_j} V_j / (e^{sink[h]} + sum_j e^{x_j}),  lse = log of the denominator.
+ * So a query sees the prefix as far as its window and its document reach.  A
+ * prefix that goes on behind the query's own document needs doc_end: without it
+ * the query also sees the prefix's part in the documents that follow.
  * A query that sees nothing gets zeros, and lse -inf without a sink (sink[h]
  * with one).  A request whose ctx_len is 0 takes no part: its rows get zeros
  * and -inf.  Rows from q_start[B] on are left as they were.  A request with
@@ -573,8 +576,9 @@ typedef struct lcsc_paged_batch {
   float* lse;                  /* [n_tokens][Hq] or NULL */
   const float* slopes;         /* [Hq] or NULL: bias by distance */
   const float* sink;           /* [Hq] or NULL */
-  const int32_t* prefix_len;   /* [B] or NULL: tokens of a prefix that every query sees whole */
+  const int32_t* prefix_len;   /* [B] or NULL: tokens of a prefix that is seen from all of its positions */
   const int32_t* doc_start;    /* [n_tokens] or NULL: first position of each row's document */
+  const int32_t* doc_end;      /* [n_tokens] or NULL: the position behind each row's document */
 } lcsc_paged_batch;
 
 int32_t lcsc_paged_attn_workspace_size(const lcsc_paged_params* p, int64_t B, int64_t n_tokens, int64_t max_new,

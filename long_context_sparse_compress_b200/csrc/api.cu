@@ -260,14 +260,14 @@ PagedForm plan_paged(const lcsc_paged_params* p, int64_t B, int64_t n_tokens, in
   float* po = cv.take<float>((size_t)2 * f.ctas * f.rows * p->head_dim);
   float* pml = cv.take<float>((size_t)2 * f.ctas * f.rows * 2);
   int32_t* meta = cv.take<int32_t>((size_t)8 * f.ctas);
-  int32_t* first = nullptr;
-  if (f.kind == 2) first = cv.take<int32_t>((size_t)(n_tokens * (p->n_heads / p->n_kv_heads) / f.rows + B));
+  int2* ends = nullptr;
+  if (f.kind == 2) ends = cv.take<int2>((size_t)(n_tokens * (p->n_heads / p->n_kv_heads) / f.rows + B));
   if (L) {
     L->part_o = po;
     L->part_ml = pml;
     L->meta = meta;
     L->ctas = f.ctas;
-    L->first = first;
+    L->block_docs = ends;
   }
   return f;
 }
@@ -954,7 +954,8 @@ int32_t lcsc_paged_attn(const lcsc_paged_params* p, const lcsc_paged_batch* s, c
   // positions a few tiles past the last one are computed in 32 bits
   if (s->max_blocks < 1 || s->max_blocks > (INT32_MAX - (kPagedAhead - 1)) / p->page_size) return LCSC_ERR_INVALID_ARG;
   if (!s->q_start || !s->ctx_len || !s->block_table) return LCSC_ERR_INVALID_ARG;
-  const void* small[] = {s->q_start, s->ctx_len, s->block_table, s->lse, s->slopes, s->sink, s->prefix_len, s->doc_start, status};
+  const void* small[] = {s->q_start, s->ctx_len, s->block_table, s->lse, s->slopes, s->sink, s->prefix_len, s->doc_start, s->doc_end,
+                         status};
   for (const void* q : small)
     if (!aligned4(q)) return LCSC_ERR_INVALID_ARG;
   if (s->n_tokens == 0) return LCSC_OK;
@@ -990,7 +991,8 @@ int32_t lcsc_paged_attn(const lcsc_paged_params* p, const lcsc_paged_batch* s, c
   L.sink = s->sink;
   L.prefix = s->prefix_len;
   L.docs = s->doc_start;
-  if (!L.docs) L.first = nullptr;
+  L.doc_ends = s->doc_end;
+  if (!L.docs && !L.doc_ends) L.block_docs = nullptr;
   L.sm_scale = p->sm_scale;
   L.cap = p->softcap;
   L.window = p->window;

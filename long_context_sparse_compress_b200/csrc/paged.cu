@@ -512,10 +512,10 @@ __global__ void __launch_bounds__(kFmaThreads) paged_fma_kernel(const __grid_con
     int item_lo, item_hi, x;
     paged_span(a, w.p_s, paged_prefix(a, w.p_b), paged_div(a, r0), &item_lo, &x);
     paged_span(a, w.p_s, paged_prefix(a, w.p_b), paged_div(a, r0 + rows - 1), &x, &item_hi);
-    if (a.docs && w.p_s.L > 0) {  // pages before every row's document are not looked at
-      int first_doc = INT_MAX;
-      for (int i = paged_div(a, r0); i <= paged_div(a, r0 + rows - 1); ++i) first_doc = min(first_doc, a.docs[w.p_s.q0 + i]);
-      item_lo = max(item_lo, first_doc);
+    if ((a.docs || a.doc_ends) && w.p_s.L > 0) {  // pages outside every row's document are not looked at
+      const int2 d = paged_docs(a, w.p_s, paged_div(a, r0), paged_div(a, r0 + rows - 1));
+      item_lo = max(item_lo, d.x);
+      item_hi = min(item_hi, d.y);
     }
     const int32_t* table = a.table + (int64_t)w.p_b * a.max_blocks;
     __syncthreads();  // the last piece is done with shared memory
@@ -523,9 +523,8 @@ __global__ void __launch_bounds__(kFmaThreads) paged_fma_kernel(const __grid_con
       int lo = 0, hi = 0, pos = 0;
       if (tid < rows) {
         const int i = paged_div(a, r0 + tid);
-        paged_span(a, w.p_s, paged_prefix(a, w.p_b), i, &lo, &hi);
+        paged_row(a, w.p_s, paged_prefix(a, w.p_b), i, &lo, &hi);
         pos = w.p_s.L - w.p_s.n + i;
-        if (a.docs) lo = max(lo, a.docs[w.p_s.q0 + i]);
       }
       lo_s[tid] = lo, hi_s[tid] = hi, pos_s[tid] = pos;
       m_s[tid] = -INFINITY, l_s[tid] = 0.f;

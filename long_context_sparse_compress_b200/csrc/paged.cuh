@@ -42,6 +42,7 @@ struct PagedLaunch {
   const float* sink;
   const int32_t* prefix;
   const int32_t* docs;
+  const int32_t* doc_ends;
   float sm_scale, cap;
   int window;
   void* out;
@@ -53,8 +54,9 @@ struct PagedLaunch {
   float* part_ml;  // [2 * ctas][rows per item][2]: max (base-2 units), sum
   int32_t* meta;   // [ctas][8]
   int ctas;
-  // many rows: the earliest document start in a block of rows (paged_block), or null
-  int32_t* first;    // [n_tokens * G / 256 + B]
+  // many rows: the earliest document start and the latest document end in a block
+  // of rows (paged_block), or null
+  int2* block_docs;  // [n_tokens * G / 256 + B]
 };
 
 struct PagedStoreLaunch {
@@ -150,7 +152,8 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedLaunch& a, int b) {
   return s;
 }
 
-// Visible positions [lo, hi) of token i of a request (its document apart).
+// Visible positions [lo, hi) of token i of a request, its document apart
+// (paged_row has that too).
 __device__ __forceinline__ void paged_span(const PagedLaunch& a, const PagedSeq& s, int prefix, int i, int* lo,
                                            int* hi) {
   if (s.L == 0) {
@@ -160,6 +163,29 @@ __device__ __forceinline__ void paged_span(const PagedLaunch& a, const PagedSeq&
   const int p = s.L - s.n + i;
   *hi = min(s.L, max(p + 1, prefix));
   *lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
+}
+
+__device__ __forceinline__ void paged_row(const PagedLaunch& a, const PagedSeq& s, int prefix, int i, int* lo, int* hi) {
+  paged_span(a, s, prefix, i, lo, hi);
+  if (a.docs) *lo = max(*lo, a.docs[s.q0 + i]);
+  if (a.doc_ends) *hi = min(*hi, max(0, a.doc_ends[s.q0 + i]));  // (differences from it stay in 32 bits)
+}
+
+// The earliest document start and the latest document end of the tokens i0 .. i1
+// (a whole warp computes them).
+__device__ __forceinline__ int2 paged_docs(const PagedLaunch& a, const PagedSeq& s, int i0, int i1) {
+  int first = 0, last = INT_MAX;
+  if (a.docs) {
+    first = INT_MAX;
+    for (int i = i0 + (threadIdx.x & 31); i <= i1; i += 32) first = min(first, a.docs[s.q0 + i]);
+    first = __reduce_min_sync(0xffffffffu, first);
+  }
+  if (a.doc_ends) {
+    last = 0;
+    for (int i = i0 + (threadIdx.x & 31); i <= i1; i += 32) last = max(last, a.doc_ends[s.q0 + i]);
+    last = __reduce_max_sync(0xffffffffu, last);
+  }
+  return make_int2(first, last);
 }
 
 __device__ __forceinline__ int paged_prefix(const PagedLaunch& a, int b) { return a.prefix ? a.prefix[b] : 0; }
@@ -181,7 +207,11 @@ __device__ __forceinline__ void paged_tiles(const PagedLaunch& a, const PagedSeq
   if constexpr (M == kPagedManyRows) {
     // An item's units are the tiles that its documents leave (packed documents
     // under a prefix, 5 requests of 11 to 3001 tokens: 226 -> 195 us).
-    if (a.first && s.L > 0) lo = min(max(lo, a.first[paged_block(a, s, mt)]), hi - 1);
+    if (a.block_docs && s.L > 0) {
+      const int2 d = a.block_docs[paged_block(a, s, mt)];
+      lo = min(max(lo, d.x), hi - 1);
+      hi = max(min(hi, d.y), lo + 1);
+    }
   }
   *t0 = lo / TK;
   *t1 = max(*t0 + 1, (hi + TK - 1) / TK);

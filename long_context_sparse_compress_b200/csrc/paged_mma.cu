@@ -163,7 +163,7 @@ struct Waits {
 };
 
 // First and past the last position that any row of a piece sees (a whole warp
-// computes it), and the first tile of the piece that holds one (t1: none does).
+// computes it), and the tiles [t0, t1) of the piece that hold them, maybe none.
 template <int M, int TK>
 struct PieceKeys {
   int lo, hi, t0, t1;
@@ -173,12 +173,12 @@ struct PieceKeys {
     int x;
     paged_span(a, w.p_s, prefix, i0, &lo, &x);
     paged_span(a, w.p_s, prefix, i1, &x, &hi);
-    if (a.docs && w.p_s.L > 0) {
-      int d = INT_MAX;
-      for (int i = i0 + (threadIdx.x & 31); i <= i1; i += 32) d = min(d, a.docs[w.p_s.q0 + i]);
-      lo = max(lo, __reduce_min_sync(0xffffffffu, d));
+    if ((a.docs || a.doc_ends) && w.p_s.L > 0) {
+      const int2 d = paged_docs(a, w.p_s, i0, i1);
+      lo = max(lo, d.x);
+      hi = min(hi, d.y);
     }
-    t1 = w.p_t1;
+    t1 = min(w.p_t1, (hi + TK - 1) / TK);
     t0 = lo < hi ? min(t1, max(w.p_t0, lo / TK)) : t1;
   }
 };
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
     };
     while (go && w.next()) {
       const PieceKeys<NR, TK> keys(a, w);
-      if (keys.t0 >= w.p_t1) continue;
+      if (keys.t0 >= keys.t1) continue;
       // the softmax warps lay out this piece's queries after the last piece's end
       if (pend && !(go = issue_pv(n - 1))) break;
       pend = false;
@@ -498,15 +498,14 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
     while (ok && w.next()) {
       const PieceKeys<NR, TK> keys(a, w);
       const int rows = w.rows(), r0 = w.p_mt * NR;
-      const bool work = keys.t0 < w.p_t1;
+      const bool work = keys.t0 < keys.t1;
       named_sync(1, 128);  // the last piece is done with shared memory
       if (tid < NR) {
         int4 r = make_int4(0, 0, 0, 0);
         if (tid < rows) {
           const int i = paged_div(a, r0 + tid);
-          paged_span(a, w.p_s, paged_prefix(a, w.p_b), i, &r.x, &r.y);
+          paged_row(a, w.p_s, paged_prefix(a, w.p_b), i, &r.x, &r.y);
           r.z = w.p_s.L - w.p_s.n + i;
-          if (a.docs) r.x = max(r.x, a.docs[w.p_s.q0 + i]);
           if (a.slopes) r.w = __float_as_int(a.slopes[w.p_h * a.G + r0 + tid - i * a.G] * kPagedLog2e);
         }
         row_s[tid] = r;
@@ -894,17 +893,15 @@ __device__ __forceinline__ void many_rescale(uint32_t o_addr, float alpha) {
   tmem_st_wait();
 }
 
-// The earliest document start of every block of rows, a warp per block.
-__global__ void __launch_bounds__(256) paged_first_kernel(const PagedLaunch a) {
+// The earliest document start and the latest end of every block of rows, a warp per block.
+__global__ void __launch_bounds__(256) paged_docs_kernel(const PagedLaunch a) {
   grid_dep_wait();
   const int b = blockIdx.x, lane = threadIdx.x & 31;
   const PagedSeq s = paged_seq(a, b);
   for (int mt = blockIdx.y * 8 + threadIdx.x / 32; (int64_t)mt * kManyRows < (int64_t)s.n * a.G; mt += gridDim.y * 8) {
     const int i0 = paged_div(a, mt * kManyRows), i1 = paged_div(a, min(s.n * a.G, (mt + 1) * kManyRows) - 1);
-    int d = INT_MAX;
-    for (int i = i0 + lane; i <= i1; i += 32) d = min(d, a.docs[s.q0 + i]);
-    d = __reduce_min_sync(0xffffffffu, d);
-    if (lane == 0) a.first[paged_block(a, s, mt)] = d;
+    const int2 d = paged_docs(a, s, i0, i1);
+    if (lane == 0) a.block_docs[paged_block(a, s, mt)] = d;
   }
 }
 
@@ -1006,7 +1003,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     int n = 0, pieces[2] = {0, 0}, cnt[2] = {0, 0};
     while (go && w.next()) {
       const PieceKeys<M, TK> keys(a, w);
-      if (keys.t0 >= w.p_t1) continue;
+      if (keys.t0 >= keys.t1) continue;
       const bool shared = w.rows() <= 128;  // both warpgroups on one tile of rows
       if (!(go = wait(&q_full[0], (uint32_t)pieces[0]++ & 1u))) break;
       if (!shared && !(go = wait(&q_full[1], (uint32_t)pieces[1]++ & 1u))) break;
@@ -1071,7 +1068,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     bool ok = true;
     while (ok && w.next()) {
       const PieceKeys<M, TK> keys(a, w);
-      if (keys.t0 >= w.p_t1) {
+      if (keys.t0 >= keys.t1) {
         // nothing to do, but the piece counts
         ok = named_and(2, 128, true);
         if (pieces > 0) ok = named_and(2, 128, wait(piece_done, (uint32_t)(pieces - 1) & 1u));
@@ -1083,7 +1080,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       // the largest scale of the piece's pages, by page numbers: 128 pages on, a
       // position may pass 2^31
       int top = 0;
-      const int last = (min(keys.hi, w.p_t1 * TK) - 1) >> a.page_log2;
+      const int last = (min(keys.hi, keys.t1 * TK) - 1) >> a.page_log2;
       for (int pg = (max(keys.t0 * TK, keys.lo) >> a.page_log2) + tid - 256; pg <= last; pg += 128) {
         const int64_t ph = pages.place(pages.entry(keys.t0, pg << a.page_log2));
         if (ph >= 0) top = max(top, __float_as_int(a.v_scale[ph]));
@@ -1204,12 +1201,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       ManyRow r = {0, INT_MAX, 1 << 30, 0.f, 0.f};  // a row that is not there sees everything and bears no bias
       if (mine) {
         const int i = paged_div(a, row);
-        paged_span(a, w.p_s, paged_prefix(a, w.p_b), i, &r.lo, &r.hi);
+        paged_row(a, w.p_s, paged_prefix(a, w.p_b), i, &r.lo, &r.hi);
         r.pos = w.p_s.L - w.p_s.n + i;
-        if (a.docs) r.lo = max(r.lo, a.docs[w.p_s.q0 + i]);
         if (a.slopes) r.slope = a.slopes[w.p_h * a.G + row - i * a.G] * kPagedLog2e;
       }
-      const bool work = keys.t0 < w.p_t1;
+      const bool work = keys.t0 < keys.t1;
       if (work) {
         // The tile's query terms: LPR lanes read a row together, 8 dims each (a
         // thread per row: 32 lines a load, five draft tokens 187 against 178 us).
@@ -1487,9 +1483,9 @@ cudaError_t launch_few(const PagedLaunch& a, const CUtensorMap& k, const CUtenso
 
 template <int D>
 cudaError_t launch_many(const PagedLaunch& a, const CUtensorMap& k, cudaStream_t stream) {
-  if (a.docs) {
+  if (a.block_docs) {
     const int64_t y = (a.n_tokens * a.G / kManyRows + 8) / 8;
-    const cudaError_t e = launch_pdl(paged_first_kernel, dim3(a.B, (unsigned)(y < 64 ? y : 64)), dim3(256), 0, stream, a);
+    const cudaError_t e = launch_pdl(paged_docs_kernel, dim3(a.B, (unsigned)(y < 64 ? y : 64)), dim3(256), 0, stream, a);
     if (e != cudaSuccess) return e;
   }
   auto kern = a.cap > 0.f || a.slopes ? paged_many_kernel<D, true> : paged_many_kernel<D, false>;

@@ -13,7 +13,7 @@ from . import workloads
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblcsc.so")
-ABI_VERSION = 4
+ABI_VERSION = 5
 
 FMT = {"f32": 0, "kv": 1, "fp8": 2, "fp4": 3}
 DT = {"f32": 0, "bf16": 1}
@@ -68,7 +68,7 @@ class PagedBatch(ctypes.Structure):
     _fields_ = [("B", c_i64), ("n_tokens", c_i64), ("max_new", c_i64), ("max_blocks", c_i64),
                 ("q_start", c_vp), ("ctx_len", c_vp), ("block_table", c_vp), ("q", c_vp), ("q_stride", c_i64),
                 ("out", c_vp), ("lse", c_vp), ("slopes", c_vp), ("sink", c_vp), ("prefix_len", c_vp),
-                ("doc_start", c_vp)]
+                ("doc_start", c_vp), ("doc_end", c_vp)]
 
 
 _SIGS = {
@@ -559,7 +559,7 @@ def paged_attn_workspace(p, B, n_tokens, max_new):
 
 
 def paged_attn(p, q, cache, block_table, ctx_len, q_start, max_new, out, lse=None, slopes=None, sink=None,
-               prefix_len=None, doc_start=None, ws=None, status=None, stream=None):
+               prefix_len=None, doc_start=None, ws=None, status=None, stream=None, doc_end=None):
     """lcsc_paged_attn: queries [tokens][n_heads][head_dim] (the token stride
     is free) over the cached tokens of their requests."""
     pool, arg = _pool_of(p, cache), _Args(stream, cache)
@@ -573,7 +573,7 @@ def paged_attn(p, q, cache, block_table, ctx_len, q_start, max_new, out, lse=Non
         B, n, max_new, block_table.shape[1], dense("q_start", q_start, _I32, B + 1), dense("ctx_len", ctx_len, _I32),
         dense("block_table", block_table, _I32), qp, qs, dense("out", out, q.dtype),
         dense("lse", lse, _F32, n * heads), dense("slopes", slopes, _F32, heads), dense("sink", sink, _F32, heads),
-        dense("prefix_len", prefix_len, _I32, B), dense("doc_start", doc_start, _I32, n))
+        dense("prefix_len", prefix_len, _I32, B), dense("doc_start", doc_start, _I32, n), dense("doc_end", doc_end, _I32, n))
     st, handle = dense("status", status, _I32), None
     if ws is None:
         handle = arg.handle()

@@ -86,7 +86,7 @@ def store(codes, scale, x, slots, page):
 
 
 def attention(q, k, v, k_scale, v_scale, table, ctx, q_start, sm_scale, window=0, cap=0.0, slopes=None, sink=None,
-              prefix=None, docs=None):
+              prefix=None, docs=None, ends=None):
     """(out, lse, bound) of every row of every request; rows of no request stay
     NaN.  bound[row, head] is the largest sum_d |q_d K_d| over the visible keys, and
     vmax[row, head] their largest |V|, for error bounds."""
@@ -116,6 +116,8 @@ def attention(q, k, v, k_scale, v_scale, table, ctx, q_start, sm_scale, window=0
                     seen &= j > p - window
                 if docs is not None:
                     seen &= j >= docs[r0 + i]
+                if ends is not None:
+                    seen &= j < ends[r0 + i]
                 for h in range(g * G, (g + 1) * G):
                     row = q[r0 + i, h].astype(np.float64)
                     x = K[seen] @ row * sm_scale

@@ -186,6 +186,65 @@ def test_requests_whose_documents_begin_behind_the_last_token(cuda_lib, dtype, n
     c.run(docs=docs).check(docs=docs)
 
 
+# ------------------------------------------------------- documents with an end
+
+def run_with_ends(c, ends, max_new=None, table=None, **kw):
+    c.run(max_new=max_new, table=table, **kw)
+    c.out.fill_(77), c.lse.fill_(77), c.status.zero_()
+    L.paged_attn(*c.pos, **{**c.args, "doc_end": i32(ends)})
+    return c.check(ends=ends, **kw)
+
+
+@pytest.mark.parametrize("dtype,cap", [(F32, 5.0), (BF16, 0.0), (BF16, 5.0)])
+@pytest.mark.parametrize("Hq,Hkv,D,P", [(12, 4, 64, 16), (8, 1, 128, 128)])
+def test_packed_documents_with_ends_under_a_prefix(cuda_lib, dtype, cap, Hq, Hkv, D, P):
+    """No query sees another document, however far the prefix goes; blocks of
+    rows whose documents end tiles before the prefix does, chunks that begin
+    inside a document, single tokens and requests without new ones."""
+    new = [700, 1, 0, 257, 300] if dtype == BF16 else [150, 1, 0, 57, 60]
+    ctx = np.array([700, 900, 40, 300, 700] if dtype == BF16 else [150, 400, 40, 90, 260])
+    c = Case(ctx, new, Hq, Hkv, D, P, dtype, seed=41)
+    pos = np.concatenate([t - n + np.arange(n) for t, n in zip(ctx, new)] + [np.zeros(c.N - sum(new), int)])
+    every = np.repeat([40, 333, 7, 90, 257], new)
+    every = np.concatenate([every, np.full(c.N - len(every), 9)])
+    starts = (pos // every * every).astype(np.int32)
+    ends = (starts + every).astype(np.int32)
+    for prefix in (ctx, ctx // 2):
+        kw = dict(docs=starts, prefix=prefix.astype(np.int32), cap=cap)
+        run_with_ends(c, ends, **kw)
+        run_with_ends(c, ends, window=33, sink=np.linspace(-2, 2, Hq).astype(np.float32), **kw)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("new", [[5, 5, 3, 1], [130, 60, 3, 1]])
+@pytest.mark.parametrize("docs", [False, True])
+def test_ends_anywhere(cuda_lib, dtype, new, docs):
+    """Ends before the query, before the first token, behind the last one and at
+    the type's least and largest numbers, with starts and without."""
+    c = Case([140, 300, 60, 7], new, 10, 2, 64, 16, dtype, seed=42)
+    rng = np.random.default_rng(9)
+    ends = rng.integers(-20, 330, c.N).astype(np.int64)
+    ends[rng.random(c.N) < 0.1] = 2 ** 31 - 1
+    ends[rng.random(c.N) < 0.1] = -2 ** 31
+    ends[c.q_start[2]:c.q_start[3]] = -2 ** 31  # a request that sees nothing
+    kw = dict(prefix=rng.integers(0, 330, 4).astype(np.int32), sink=rng.standard_normal(10).astype(np.float32),
+              slopes=np.exp2(-np.arange(10.0)).astype(np.float32))
+    if docs:
+        kw["docs"] = rng.integers(-5, 200, c.N).astype(np.int32)
+    run_with_ends(c, ends.astype(np.int32), **kw)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("new", [[4, 5], [60, 70]])
+def test_ends_pass_over_pages_behind_them(cuda_lib, dtype, new):
+    """Pages behind every row's document may be missing, under a prefix that goes on."""
+    c = Case([300, 500], new, 8, 2, 128, 16, dtype, seed=43)
+    ends = np.concatenate([np.repeat([100, 333], new), np.zeros(c.N - sum(new), int)]).astype(np.int32)
+    table = c.table.copy()
+    table[0, -(-100 // 16):19], table[1, -(-333 // 16):32] = -1, c.n_pages + 5
+    run_with_ends(c, ends, table=table, prefix=np.array([300, 480], np.int32))
+
+
 # ------------------------------------------------------------------- sinks
 
 @pytest.mark.parametrize("dtype", [F32, BF16])

@@ -2,7 +2,9 @@
 import ctypes
 
 import pytest
+import torch
 
+from long_context_sparse_compress_b200 import lib as L
 from tests.test_paged_args import INVALID, WORKSPACE, attn, good_batch, good_params, good_pool, lib  # noqa: F401
 
 
@@ -48,3 +50,15 @@ def test_status_words_of_no_alignment(lib):  # noqa: F811
         assert lib.lcsc_paged_attn(ctypes.byref(p), ctypes.byref(b), ctypes.byref(c), 4096, 1 << 40, status, None) == INVALID
         assert lib.lcsc_paged_store(ctypes.byref(p), ctypes.byref(c), 16, 256, 32, 256, 16, 1, status, None) == INVALID
         assert lib.lcsc_page_plan(64, 3, 5, 4, 10, *(1 << k for k in range(10, 20)), 256, out.value, status, None) == INVALID
+
+
+def test_document_ends(lib):  # noqa: F811
+    """Their alignment, and in the Python layer their type and size."""
+    assert attn(lib, good_params(), good_batch(doc_end=5), good_pool()) == INVALID
+    assert attn(lib, good_params(), good_batch(doc_end=4), good_pool(), None) == WORKSPACE
+    p, cache = L.paged_params(4, 2, 64, 16), L.PagedCache(3, 2, 16, 64, device="cpu")
+    q, i = torch.zeros((5, 4, 64), dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    for ends in (torch.zeros(5), torch.zeros(4, dtype=torch.int32), torch.zeros(5, dtype=torch.int64)):
+        with pytest.raises(L.LcscError, match="doc_end"):
+            L.paged_attn(p, q, cache, torch.zeros((2, 3), dtype=torch.int32), i, torch.zeros(3, dtype=torch.int32), 1,
+                         torch.zeros_like(q), doc_end=ends)
