@@ -521,11 +521,12 @@ int32_t lcsc_page_plan(int32_t page_size, int64_t B, int64_t n_tokens, int64_t m
  * the scale grows; code = E4M3_rne(x / s').  Rows of a page after the new ones
  * keep their codes.  A value that is not finite is stored as 0 and left out of
  * amax (LCSC_DEV_RANGE).
- * The tokens of one page are adjacent and in rising slot order, as
- * lcsc_page_plan gives them.  A slot outside the pool, or one that follows its
- * neighbour within a page out of that order (the same slot twice, say), is
- * skipped (LCSC_DEV_BAD_INDEX); a page visited again further on gets one
- * visit's rows or the other's in each place. */
+ * The tokens of one page are adjacent and their slots rise by one, as
+ * lcsc_page_plan gives them.  A slot outside the pool is skipped, and one that
+ * follows its neighbour within a page out of that order (the same slot twice, say)
+ * or behind skipped rows, with those that go on from it (LCSC_DEV_BAD_INDEX).  A
+ * page that comes again behind rows of another one, or that two calls at once
+ * write, is left with codes and a scale that need not belong together. */
 int32_t lcsc_paged_store(const lcsc_paged_params* p, const lcsc_paged_cache* cache, const void* k, int64_t k_stride,
                          const void* v, int64_t v_stride, const int32_t* slots, int64_t n_tokens,
                          int32_t* status, void* stream);

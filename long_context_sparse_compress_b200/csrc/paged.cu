@@ -336,13 +336,18 @@ __global__ void __launch_bounds__(kStoreWarps * 32) paged_store_kernel(PagedStor
   {
     const int64_t t = t0 + tid;
     int32_t s = -1, before = -1;
+    bool gap = false;
     if (tid < kLook && t < a.n_tokens) {
       s = a.slots[t];
       if (t > 0) before = a.slots[t - 1];
+      // behind skipped rows it is the last one before them that may have the page
+      gap = s >= 0 && t > 0 && before < 0;
+      if (gap)
+        for (int64_t u = t - 2; u >= 0 && u > t - kMaxPage && before < 0; --u) before = a.slots[u];
     }
     if (tid < kLook) slot_s[tid] = s;
     const bool same = s >= 0 && before >= 0 && (s >> a.page_log2) == (before >> a.page_log2);
-    const bool on = same && s == before + 1;
+    const bool on = same && !gap && s == before + 1;
     bool start = s >= 0 && !on && tid < TILE;
     // out of order within a page, or past the pool
     if (start && (same || (s >> a.page_log2) >= a.n_pages)) start = false, bits |= LCSC_DEV_BAD_INDEX;

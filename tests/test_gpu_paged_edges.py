@@ -19,6 +19,31 @@ def set_page(codes, scale, page, values):
     codes[page] = formats.e4m3_encode(values / s[:, None, None])
 
 
+# ------------------------------------------------------------------- store
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("P,holes", [(16, 1), (128, 1), (128, 100)])
+def test_store_skips_what_comes_behind_a_hole_in_a_page(cuda_lib, dtype, P, holes):
+    """Rows of a page behind skipped ones would be a second visit beside the
+    first, with a scale of its own: they are skipped and reported; other pages
+    behind skipped rows are stored."""
+    rng = np.random.default_rng(P + holes)
+    slots = np.concatenate([[3 * P + 1, 3 * P + 2], [-1] * holes, 3 * P + 3 + holes + np.arange(4) % (P - 3 - holes),
+                            [-1], np.arange(5 * P, 6 * P), [-1] * 130, [2 * P + 5]]).astype(np.int32)
+    x = torch.from_numpy(rng.standard_normal((len(slots), 2, 64)).astype(np.float32)).to(dtype)
+    x[2 + holes:6 + holes] *= 64
+    codes, scale = (rng.integers(0, 0x7E, (7, 2, P, 64)).astype(np.uint8), np.exp2(rng.integers(-9, 3, (7, 2))).astype(np.float32))
+    cache = L.PagedCache.of(*(torch.from_numpy(codes).cuda() for _ in "kv"), *(torch.from_numpy(scale).cuda() for _ in "kv"))
+    st = status0()
+    L.paged_store(L.paged_params(2, 2, 64, P, x_dtype="f32" if dtype == F32 else "bf16"), cache, x.cuda(), x.cuda(),
+                  i32(slots), status=st)
+    assert st.item() == L.DEV_BAD_INDEX
+    slots[2 + holes:6 + holes] = -1
+    paged.store(codes, scale, x.float().numpy(), slots, P)
+    for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        assert np.array_equal(s.cpu().numpy(), scale) and np.array_equal(c.cpu().numpy(), codes)
+
+
 # ------------------------------------------------------- V scales far apart
 
 @pytest.mark.parametrize("dtype,form,ratio", [(F32, FEW, 2.0 ** -30)] + [
