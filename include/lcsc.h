@@ -485,12 +485,15 @@ typedef struct lcsc_paged_cache {
  * already cached, and its new ones; n_new < 0: the request has ended.
  *   block_table [B][max_blocks] (in, out): the first ceil(cached / P) entries
  *     of a row are its pages; entries for the new tokens are filled in, no
- *     other is touched.
- *   free_pages [n_pages] (in, out): a stack of n_free[0] free pages.  The
- *     pages of the ended requests go on top of it first, in request order;
- *     then the requests take the pages they need from the top, in request
- *     order.  n_free_out[0]: the stack's height afterwards (may be n_free
- *     itself; where it is not, calling again with the same n_free gives the
+ *     other is touched.  (Where cached falls, as behind draft tokens that were not
+ *     taken, the pages behind the first ceil(cached / P) are the caller's to put
+ *     back on the stack.)
+ *   free_pages [n_pages] (in, out): a stack of n_free[0] free pages; what lies
+ *     above it is not kept.  The pages of the ended requests go on top of it first,
+ *     in request order, but for entries below 0 (pages released before, as those
+ *     left of every window); then the requests take the pages they need from the
+ *     top, in request order.  n_free_out[0]: the stack's height afterwards (may be
+ *     n_free itself; where it is not, calling again with the same n_free gives the
  *     same plan).
  *   ctx_len [B] = cached + n_new; q_start [B + 1]: first row of each request;
  *   slots, positions (nullable) [n_tokens]: of each row its slot, page * P +

@@ -32,7 +32,7 @@ class Plan:
         self.no_pages = self.bad_length = False
         for b in range(B):
             if n_new[b] < 0:
-                stack += list(table[b, :-(-int(cached[b]) // page)])
+                stack += [x for x in table[b, :-(-int(cached[b]) // page)] if x >= 0]
         self.free[:len(stack)] = stack
         row, starved = 0, False
         for b in range(B):

@@ -5,7 +5,7 @@ import torch
 
 from long_context_sparse_compress_b200 import lib as L
 from oracle import formats, paged
-from tests.test_gpu_paged import BF16, F32, Case, i32, status0
+from tests.test_gpu_paged import BF16, F32, Case, check_plan, i32, run_plan, status0
 
 pytestmark = pytest.mark.gpu
 
@@ -17,6 +17,34 @@ def set_page(codes, scale, page, values):
     s = np.vectorize(paged.scale_of)(np.abs(values).max((1, 2)))
     scale[page] = s
     codes[page] = formats.e4m3_encode(values / s[:, None, None])
+
+
+# -------------------------------------------------------------------- plan
+
+@pytest.mark.parametrize("width", [3, 70, 1200])
+def test_ended_requests_whose_early_pages_were_released(cuda_lib, width):
+    """Entries below 0 do not come back to the stack; the others do, in their order."""
+    rng = np.random.default_rng(width)
+    B, P = 70, 16
+    cached = rng.integers(1, width * P + 1, B)
+    n_new = np.where(np.arange(B) % 3 == 0, 2, -1)
+    cached = np.where(n_new < 0, cached, np.minimum(cached, width * P - 2))
+    have = -(-cached // P)
+    table = np.full((B, width), -1)
+    pages = iter(rng.permutation(int(have.sum()) + 100))
+    for b in range(B):
+        for col in range(have[b]):
+            gone = n_new[b] < 0 and (col < have[b] // 2 if b % 2 else rng.random() < 0.3)
+            table[b, col] = -1 if gone else next(pages)
+    rest = list(pages)
+    free = np.array(rest + [-3] * (int(have.sum()) + 100 - len(rest)))
+    args = (P, cached, n_new, table, free, len(rest), int(np.maximum(n_new, 0).sum()))
+    want = paged.Plan(*args)
+    assert not want.no_pages and -1 not in want.free[:len(rest)]
+    got = run_plan(*args)
+    top = len(rest) + int(((table >= 0) & (n_new < 0)[:, None]).sum())
+    got["free"][top:] = i32(want.free[top:])  # above the stack
+    check_plan(got, want)
 
 
 # ------------------------------------------------------------------- store
