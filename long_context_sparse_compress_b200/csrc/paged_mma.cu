@@ -146,7 +146,9 @@ __device__ __forceinline__ bool wait_asleep(uint64_t* bar, uint32_t parity, uint
   }
 }
 
-// Bounded wait of a whole warp; false for every lane if one gave up or the CTA has.
+// Bounded wait of a whole warp; false for every lane if one gave up or the CTA
+// has.  What comes behind the first look at the barrier is out of line (chunk of
+// 4096 tokens: 1,059 us with it in line, 1,036 so).
 struct Waits {
   int32_t* status;
   uint64_t limit_ns;
@@ -154,6 +156,10 @@ struct Waits {
   uint32_t ns;  // of sleep between polls
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
     if (__all_sync(0xffffffffu, !*abort && mbar_try_wait(bar, parity))) return true;
+    return longer(bar, parity, ns, status, limit_ns, abort);
+  }
+  static __device__ __noinline__ bool longer(uint64_t* bar, uint32_t parity, uint32_t ns, int32_t* status,
+                                             uint64_t limit_ns, volatile int* abort) {
     // (one vote, as lanes apart could read the flag before and after it is set)
     if (__any_sync(0xffffffffu, *abort)) return false;
     const bool ok = __all_sync(0xffffffffu, wait_asleep(bar, parity, ns, status, limit_ns));
