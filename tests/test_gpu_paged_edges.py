@@ -298,6 +298,31 @@ def test_ends_pass_over_pages_behind_them(cuda_lib, dtype, new):
     run_with_ends(c, ends, table=table, prefix=np.array([300, 480], np.int32))
 
 
+# -------------------------------------------------------- parts of a batch
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_call_for_each_kind_of_request(cuda_lib, dtype):
+    """Decodes and prompts of one batch in calls of their own, over slices of its
+    arrays: each writes its requests' rows and no other."""
+    c = Case([300, 170, 65, 200, 90], [1, 1, 1, 130, 77], 8, 2, 128, 32, dtype, seed=44)
+    prefix = np.array([0, 100, 0, 150, 90], np.int32)
+    c.run(prefix=prefix).check(prefix=prefix)
+    p, q, cache, table, ctx, q_start, _, out = c.pos
+    for first, last, hint in ((3, 5, 130), (0, 3, 1)):
+        out.fill_(77), c.lse.fill_(77), c.status.zero_()
+        L.paged_attn(p, q, cache, table[first:last], ctx[first:last], q_start[first:last + 1], hint, out, c.lse,
+                     prefix_len=c.args["prefix_len"][first:last], status=c.status)
+        rows = slice(int(c.q_start[first]), int(c.q_start[last]))
+        kept, kept_lse = out[rows].clone(), c.lse[rows].clone()
+        out[rows], c.lse[rows] = 77, 77
+        assert (out == 77).all() and (c.lse == 77).all()
+        c.run(prefix=prefix, max_new=hint)  # the whole batch in the same form
+        torch.cuda.synchronize()
+        c.out[rows], c.lse[rows] = kept, kept_lse
+        c.check(prefix=prefix)
+        p, q, cache, table, ctx, q_start, _, out = c.pos
+
+
 # ------------------------------------------------------------------- sinks
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
