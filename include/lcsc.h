@@ -444,7 +444,8 @@ int32_t lcsc_attn_merge(const lcsc_params* p, int32_t n_parts, const void* part_
  * Ordinary attention over the raw tokens of many requests of different
  * lengths, for what a server runs beside the compressed layers: short
  * contexts ("How DeepSeek V4 Handles 1M Token Context": below about 8K tokens
- * plain attention wins) and plain or sliding-window layers of the same stack.
+ * plain attention wins) and plain or sliding-window layers with heads of 64 or
+ * 128 values.
  * K and V lie in pages of P tokens in E4M3, with one float32 scale for each
  * page and KV head.  One serving step is
  *   lcsc_page_plan   block table, slots and lengths from the requests' token counts;
@@ -454,7 +455,8 @@ int32_t lcsc_attn_merge(const lcsc_params* p, int32_t n_parts, const void* part_
  * request b has the rows q_start[b] .. q_start[b + 1] - 1.  ctx_len is the
  * array that the other calls of this library take (length after the step).
  * The pool (dev): k, v [n_pages][Hkv][P][D] E4M3 codes, 16-byte aligned;
- * k_scale, v_scale [n_pages][Hkv] float32.  Token t of a request lies at row
+ * k_scale, v_scale [n_pages][Hkv] float32, powers of two as the store writes them
+ * (of other numbers the tensor cores keep 11 bits for V).  Token t of a request lies at row
  * t % P of page block_table[b][t / P]; its value is code * scale.  The int32 and
  * float32 arrays of this section need the alignment of their type only.
  * Scale rule: the least power of two s with amax <= 448 s (not below 2^-100).
@@ -569,7 +571,10 @@ int32_t lcsc_paged_store(const lcsc_paged_params* p, const lcsc_paged_cache* cac
 typedef struct lcsc_paged_batch {
   int64_t B, n_tokens;
   int64_t max_new;             /* >= 1: the most new tokens of one request, if known, else n_tokens; it decides
-                                  the kernel's form only: no result depends on its being right */
+                                  the kernel's form only: any value gives every row its result (within the
+                                  precision above).  A call has one form: single tokens beside a prompt take
+                                  the prompt's, which may double their time; a call for each kind, over its
+                                  requests' part of the arrays of B, is faster */
   int64_t max_blocks;          /* block_table row length; max_blocks * P <= 2^31 - 4096 */
   const int32_t* q_start;      /* [B + 1] */
   const int32_t* ctx_len;      /* [B] */

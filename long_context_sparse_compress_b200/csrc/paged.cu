@@ -5,8 +5,7 @@
 //
 // Plain attention over raw tokens stands beside the compressed layers: "How
 // DeepSeek V4 Handles 1M Token Context" (docs.bswen.com) puts the crossover of
-// the compressed form at about 8K tokens, and the stack has a sliding-window
-// layer of its own.
+// the compressed form at about 8K tokens.
 #include <type_traits>
 
 #include "kernels.cuh"

@@ -207,7 +207,7 @@ __device__ __forceinline__ void paged_tiles(const PagedLaunch& a, const PagedSeq
   paged_span(a, s, prefix, paged_div(a, min(rows, (mt + 1) * M) - 1), &x, &hi);
   if constexpr (M == kPagedManyRows) {
     // An item's units are the tiles that its documents leave (packed documents
-    // under a prefix, 5 requests of 11 to 3001 tokens: 226 -> 195 us).
+    // under a prefix, 5 requests of 11 to 3001 tokens: 14% less time).
     if (a.block_docs && s.L > 0) {
       const int2 d = a.block_docs[paged_block(a, s, mt)];
       lo = min(max(lo, d.x), hi - 1);

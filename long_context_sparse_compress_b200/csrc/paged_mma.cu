@@ -259,7 +259,7 @@ struct PageAhead {
 // 5 x 16 KB of operands (640 cycles of shared memory at D = 128 against 1,420
 // cycles of HBM time); two CTAs per SM overlap one's softmax with the other's
 // copies and products.  16 requests of 16K to 64K tokens, 64 heads on 8, D = 128:
-// 204 us, 5.8 TB/s, 90% of the measured copy rate.
+// 233 us, 5.1 TB/s, 78% of the measured copy rate.
 
 constexpr int kFewThreads = 192;  // warps 0-3 softmax, 4 copies, 5 MMA
 constexpr int kQTerms = 2, kPTerms = 3;
@@ -725,34 +725,37 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
 // need no exchange.  O stays in TMEM; it is rescaled only when a row's maximum
 // has grown by more than 2^6.  Weights are f16 numbers from 2^15 down to steps of
 // 2^-24, the row's largest at least 2^9: 11 bits down to 2^-23 of it, and below
-// that an error of 2^-34 of it at most.  V's codes become f16 numbers exactly: four warps read them
-// from global memory a tile ahead and write code * 2^7 * (page scale /
+// that an error of 2^-34 of it at most.  V's codes become f16 numbers: four warps
+// read them from global memory a tile ahead and write code * 2^7 * (page scale /
 // largest page scale of the piece), which is exact for scales down to 2^-22 of
 // the largest and loses only what lies below 2^-32 of the largest possible |V|.
 // Two tiles keep the tensor cores busy with one while the other's weights are
 // made; a block of up to 128 rows is one tile, which the two warpgroups share by
 // taking its tiles of keys in turn and joining their O at the end (16 requests of
-// 4K to 32K tokens, 32 rows each, D = 128: 236 us, 2.4 TB/s; a million tokens for
-// 64 capped heads on one: 119 us, 2.3 TB/s; both of a CTA's chain from scores to
+// 4K to 32K tokens, 32 rows each, D = 128: 208 us, 2.7 TB/s; a million tokens for
+// 64 capped heads on one: 125 us, 2.1 TB/s; both of a CTA's chain from scores to
 // weights).
 //
 // Bound: per 256 x 128 step the products take 2,048 cycles of the tensor pipe,
 // as do the exponentials of the MUFU (32 K at 16 a cycle), and shared memory
-// about 2,900 (operands 2,048, P 512, V 256, K 128).  Measured 4,700: one
-// warpgroup's chain of waiting for its scores (700), their maxima (800), weights
-// (2,200) and the copies' bookkeeping; taking work out of the kernel shows that
-// no unit holds it (no exponentials: -2%, one query term: -4%, no V
-// conversion: -8%), while larger loop bodies cost 10 to 30% and twice the
-// softmax warps 46%.  Chunk of 4096
-// tokens on 4096 cached, 64 heads on 8, D = 128: 960 us, 0.86 PFLOP/s, 53% of the
-// measured bf16 rate.
+// about 2,900 (operands 2,048, P 512, V 256, K 128).  Measured 5,400 (the tensor
+// pipe is active 38% of the time, the MUFU 39%, issue slots 42%): one warpgroup's
+// chain of waiting for its scores, their maxima, weights and the copies'
+// bookkeeping (700, 800 and 2,200 of the cycles by clock probes).  Of 8.4 warps
+// an issue, 3.5 wait for TMEM loads or a barrier's look, 1.6 for fixed latencies,
+// 0.9 for shared memory or the MUFU and 0.3 for instructions.  Taking work out of
+// the kernel shows that no unit holds it (no exponentials: -2%, one query term:
+// -4%, no V conversion: -8%), while larger loop bodies cost 10 to 30% and twice
+// the softmax warps 46%.  Chunk of 4096 tokens on 4096 cached, 64 heads on 8,
+// D = 128: 1,040 us, 0.79 PFLOP/s, 48% of the measured bf16 rate.
 
 constexpr int kManyThreads = 448;  // warps 0-7 softmax (two tiles), 8-11 V, 12 copies, 13 MMA
 constexpr int kManyRows = kPagedManyRows;
 // A row's weights are 2^(x - reference), the reference kDrop below the row's
 // maximum when it is taken, and taken anew, with O rescaled, when a score has
-// grown past it by more than kLazy (base-2 units): f16 weights of up to 2^15.  (Chunk of
-// 4096 tokens: 1,041 us with a drop of 9 or 7, 1,051 with 11, which rescales more.)
+// grown past it by more than kLazy (base-2 units): f16 weights of up to 2^15.
+// (Chunk of 4096 tokens: 1,041 us with a drop of 9 or 7, 1,051 with 11, which
+// rescales more.)
 constexpr float kDrop = 9.f, kLazy = 15.f;
 
 template <int D>
@@ -1515,10 +1518,11 @@ cudaError_t launch_mma(const PagedLaunch& a, const PagedForm& f, const CUtensorM
 PagedForm paged_mma_form(int D, int G, int64_t max_new) {
   // Few rows: up to 16 per KV head and request.  From 17 on two warpgroups over
   // 128 rows are faster, however many of them are empty (16 requests of 4K to
-  // 32K tokens, 8 KV heads, us: D = 128, 8 rows 121 against 230, 16 rows 160
-  // against 232, 32 rows 307 with a few-rows kernel of that size against 237;
-  // D = 64, 8 rows 108 against 179, 16 rows 157 against 180, 32 rows 291
-  // against 184).
+  // 32K tokens, 8 KV heads, us: D = 128, 8 rows 110 against 201, 16 rows 146
+  // against 205, 32 rows 307 with a few-rows kernel of that size against 208;
+  // D = 64, 8 rows 99 against 165, 16 rows 143 against 166, 32 rows 291 against
+  // 170).  One form serves the call: 32 decodes at 16K to 64K tokens beside a
+  // chunk of 2048 take 2,158 us, in two calls 492 and 768.
   const int64_t rows = max_new > 16 ? 17 : max_new * G;
   if (rows > 16) return {2, kManyRows, sm_count()};
   return {1, rows <= 8 ? 8 : 16, 2 * sm_count()};
