@@ -656,7 +656,11 @@ __global__ void __launch_bounds__(kFmaThreads) paged_fma_kernel(const __grid_con
         const float s0 = s_s[r][lane], s1 = s_s[r][lane + 32];
         const float m_old = m_s[r], m_new = fmaxf(m_old, warp_max(fmaxf(s0, s1)) * factor);
         const float ref = m_new == -INFINITY ? 0.f : m_new;
-        const float p0 = paged_ex2(fmaf(s0, factor, -ref)), p1 = paged_ex2(fmaf(s1, factor, -ref));
+        // (from 2^20 on a score is rounded as the maximum was: less its unrounded
+        // self, it could pass the exponential's range)
+        const bool big = fabsf(m_new) >= 0x1p20f;
+        const float p0 = paged_ex2(big ? __fadd_rn(__fmul_rn(s0, factor), -ref) : fmaf(s0, factor, -ref));
+        const float p1 = paged_ex2(big ? __fadd_rn(__fmul_rn(s1, factor), -ref) : fmaf(s1, factor, -ref));
         const float sum = warp_sum(p0 + p1);
         p_s[lane][r] = p0 * sc_s[stage][1][lane];
         p_s[lane + 32][r] = p1 * sc_s[stage][1][lane + 32];

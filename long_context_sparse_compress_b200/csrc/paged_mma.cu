@@ -757,6 +757,7 @@ constexpr int kManyRows = kPagedManyRows;
 // (Chunk of 4096 tokens: 1,041 us with a drop of 9 or 7, 1,051 with 11, which
 // rescales more.)
 constexpr float kDrop = 9.f, kLazy = 15.f;
+constexpr float kBig = 0x1p20f;  // scores whose rounding is no small part of that range; their reference is the maximum
 
 template <int D>
 struct ManyCfg {
@@ -1300,11 +1301,19 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           const bool inside = __all_sync(0xffffffffu, r.lo <= j0 && r.hi >= j0 + TK && (lane / 8 != of4 || ks >= 0.f));
           if (!(ok = wait(&s_full[g], (uint32_t)cnt & 1u))) break;
           tc_fence_after();
-          const bool plain = !GEN && inside;  // the products are the scores but for a factor
+          bool plain = !GEN && inside;  // the products are the scores but for a factor
           float top;
-          if constexpr (GEN) top = many_top<kScores>(a, r, cap2, ks, 8 * of4, j0, inside, s_addr, h0, h1);
-          else if (plain) top = many_top<kPlain>(a, r, cap2, ks, 8 * of4, j0, inside, s_addr, h0, h1);
-          else top = many_top<kMasked>(a, r, cap2, ks, 8 * of4, j0, inside, s_addr, h0, h1);
+          if constexpr (GEN) {
+            top = many_top<kScores>(a, r, cap2, ks, 8 * of4, j0, inside, s_addr, h0, h1);
+          } else {
+            if (plain) {
+              top = many_top<kPlain>(a, r, cap2, ks, 8 * of4, j0, inside, s_addr, h0, h1);
+              // (scores from 2^20 on are rounded before the maximum is taken from
+              // them: weights of unrounded ones could pass f16's range)
+              plain = __all_sync(0xffffffffu, fabsf(top) < kBig);
+            }
+            if (!plain) top = many_top<kMasked>(a, r, cap2, ks, 8 * of4, j0, inside, s_addr, h0, h1);
+          }
           if (split) {
             float other;
             if (!(ok = swapped(top, &other))) break;
@@ -1313,11 +1322,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           const bool fresh = t == t_first;
           float alpha = 1.f;
           bool grown = false;
-          // (scores from 2^20 on are too coarse for the last part of f16's range)
-          if (top - m_ref > fmaf(fabsf(top), -0x1p-21f, kLazy) || (fresh && top > -INFINITY)) {
-            alpha = paged_ex2(m_ref - (top - kDrop));  // before the first key: 0
+          if (top - m_ref > kLazy || (fresh && top > -INFINITY)) {
+            const float ref = fabsf(top) < kBig ? top - kDrop : top;
+            alpha = paged_ex2(m_ref - ref);  // before the first key: 0
             grown = !fresh;
-            m_ref = top - kDrop;
+            m_ref = ref;
             l *= alpha;
           }
           // P and O: the last tile's P V has read and added to them

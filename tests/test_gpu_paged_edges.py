@@ -193,6 +193,20 @@ def test_queries_near_the_least_magnitude(cuda_lib, dtype, new, form):
     c.run(max_new=form).check()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("new,form", [([1, 3], FEW), ([1, 3], MANY), ([160, 200], 200)])
+@pytest.mark.parametrize("exponent", [16, 24, 27, 34, 60])
+def test_scores_of_any_size(cuda_lib, dtype, new, form, exponent):
+    """Scores of 2^18 to 2^62: the softmax is all on the largest, and what is
+    left of float32's bits decides which, but it is a number."""
+    c = Case([1500, 240], new, 8, 2, 64, 16, dtype, seed=39)
+    c.ks *= np.float32(2.0 ** exponent)
+    c.run(max_new=form).check()
+    live = int(c.q_start[-1])
+    assert torch.isfinite(c.out[:live]).all() and torch.isfinite(c.lse[:live]).all()
+    assert (c.out[:live].float().abs().amax(2) > 0).all()
+
+
 # ------------------------------------------------- what no query of a step sees
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
