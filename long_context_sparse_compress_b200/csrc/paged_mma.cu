@@ -259,7 +259,7 @@ struct PageAhead {
 // 5 x 16 KB of operands (640 cycles of shared memory at D = 128 against 1,420
 // cycles of HBM time); two CTAs per SM overlap one's softmax with the other's
 // copies and products.  16 requests of 16K to 64K tokens, 64 heads on 8, D = 128:
-// 233 us, 5.1 TB/s, 78% of the measured copy rate.
+// 217 us, 5.4 TB/s, 84% of the measured copy rate.
 
 constexpr int kFewThreads = 192;  // warps 0-3 softmax, 4 copies, 5 MMA
 constexpr int kQTerms = 2, kPTerms = 3;
@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
 // made; a block of up to 128 rows is one tile, which the two warpgroups share by
 // taking its tiles of keys in turn and joining their O at the end (16 requests of
 // 4K to 32K tokens, 32 rows each, D = 128: 208 us, 2.7 TB/s; a million tokens for
-// 64 capped heads on one: 125 us, 2.1 TB/s; both of a CTA's chain from scores to
+// 64 capped heads on one: 120 us, 2.2 TB/s; both of a CTA's chain from scores to
 // weights).
 //
 // Bound: per 256 x 128 step the products take 2,048 cycles of the tensor pipe,
@@ -747,7 +747,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, NR>::kPerSm))
 // the kernel shows that no unit holds it (no exponentials: -2%, one query term:
 // -4%, no V conversion: -8%), while larger loop bodies cost 10 to 30% and twice
 // the softmax warps 46%.  Chunk of 4096 tokens on 4096 cached, 64 heads on 8,
-// D = 128: 1,040 us, 0.79 PFLOP/s, 48% of the measured bf16 rate.
+// D = 128: 1,010 us, 0.82 PFLOP/s, 50% of the measured bf16 rate.
 
 constexpr int kManyThreads = 448;  // warps 0-7 softmax (two tiles), 8-11 V, 12 copies, 13 MMA
 constexpr int kManyRows = kPagedManyRows;
@@ -1531,7 +1531,7 @@ PagedForm paged_mma_form(int D, int G, int64_t max_new) {
   // against 205, 32 rows 307 with a few-rows kernel of that size against 208;
   // D = 64, 8 rows 99 against 165, 16 rows 143 against 166, 32 rows 291 against
   // 170).  One form serves the call: 32 decodes at 16K to 64K tokens beside a
-  // chunk of 2048 take 2,158 us, in two calls 492 and 768.
+  // chunk of 2048 take 2,138 us, in two calls 467 and 712.
   const int64_t rows = max_new > 16 ? 17 : max_new * G;
   if (rows > 16) return {2, kManyRows, sm_count()};
   return {1, rows <= 8 ? 8 : 16, 2 * sm_count()};
