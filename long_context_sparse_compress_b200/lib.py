@@ -416,6 +416,8 @@ def attn_merge(p, part_out, part_lse, sink, ctx_len, out, lse=None, stream=None)
 
 
 # -------------------------------------------------- paged 8-bit cache of raw tokens
+# With `stream`, the tensors given stay the caller's to keep, or to record on that
+# stream, until the call has run; a workspace that a call makes needs neither.
 
 def paged_params(n_heads, n_kv_heads, head_dim, page_size, sm_scale=None, q_dtype="bf16", x_dtype="bf16", window=0,
                  softcap=0.0):
